@@ -44,39 +44,43 @@ __device__ __forceinline__ uint4 e4m3x16(const float (&p)[16]) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&v)[16]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[8], float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
     v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
   }
 }
-__device__ __forceinline__ uint32_t abs_max16(const float (&v)[16]) {
-  uint32_t m = 0;                                        // (shifted: without the sign, in the same order)
+// The largest magnitude; NaN where there is one (three operands a step).
+__device__ __forceinline__ float abs_max16(const float (&v)[16]) {
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) m = __vimax3_u32(m, __float_as_uint(v[i]) << 1, __float_as_uint(v[i + 1]) << 1);
-  return m >> 1;
+  for (int i = 1; i < 15; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
+  asm("max.NaN.abs.f32 %0, %0, %1, %1;" : "+f"(m) : "f"(v[15]));
+  return m;
 }
 
 // 16 BF16 values; WIDE: from a 32-byte boundary, in one load.
 template <bool WIDE>
-__device__ __forceinline__ void load16(const uint16_t* p, float (&v)[16]) {
-  uint4 a, b;
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
   if (WIDE) {
     asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p));
   } else {
-    a = __ldg(reinterpret_cast<const uint4*>(p));
-    b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
-  unpack16(a, b, v);
 }
 
 // silu(g) u for a BF16 g.  log2(e) = kHi + kLo with 15 bits in kHi: g kHi is exact, and 2^(-g kLo) = 1 - g kLo ln 2
-// within 2^-24 while |g| < 60 (above, e^-g is nothing beside 1; below, the result is under 2^-80).  Then 1 + e^-g
-// is off by 2^-22 (ex2.approx) and two roundings, its reciprocal by 2^-23 more, and two products: 5 x 2^-23 together.
+// within 0.8 x 2^-24 while |g| <= 60 (above, e^-g is nothing beside 1).  Then 1 + e^-g is off by 2^-22 (ex2.approx),
+// that and two roundings, its reciprocal by 2^-23 more, and two products: 5.4 x 2^-23 together.  Below -60 the value is
+// under 2^-81 |u| and less exact, and from -87.5 on it is lost: the reciprocal, under 2^-126, comes as 0.  That is
+// nothing beside a block's maximum (less than half of the least code's step), unless |u| is 2^62 times as large as
+// the maximum.  The kernel looks for such an up.
+constexpr float kEnd = -60.0f, kLost = 0x1p62f;
 __device__ __forceinline__ float silu_near(float g, float u) {
   constexpr float kHi = 0x1.7154p+0f, kLoLn2 = 4.8884952e-06f;
   float e, s;
@@ -85,7 +89,7 @@ __device__ __forceinline__ float silu_near(float g, float u) {
   return g * s * u;
 }
 // A product's distance from the border between two codes that it is in doubt about: the 20 bits below a code's
-// three, off by 5 + 5 (value and maximum) + 1 (two roundings) times 2^-23 of a mantissa below 2, so 22 at most.
+// three, off by 5.4 + 5.4 (value and maximum) + 1 (two roundings) times 2^-23 of a mantissa below 2, so 23.6 at most.
 // (Below 2^-6, where codes are subnormal, the borders lie elsewhere; such values are taken as they are.)  With 16
 // values a lane some 2 % of the warps are in doubt.
 constexpr uint32_t kDoubt = 24, kDoubtful = 2 * kDoubt << 12;
@@ -100,18 +104,25 @@ __device__ __noinline__ double silu64(uint16_t gate, uint16_t up) {
 }
 
 // Codes in doubt, decided in 64 bits by the block's eight threads (every thread of the warp calls): the maximum
-// from the values near it, then the codes.  all: every value is in doubt, and the scale is formed again too.  A
-// product is rounded to f32 by way of an odd last bit, so that the rounding to a code decides as one would.
+// from the values near it, then the codes.  all, or a value of the block that silu_near may have lost: every value is in doubt,
+// and the scale is formed again too.  A product is rounded to f32 by way of an odd last bit, so that the rounding to
+// a code decides as one would.
 __device__ __noinline__ void settle(const uint16_t* gate, const uint16_t* up, bool have, float most, float f, bool all,
                                     uint4& code, float& scale) {
   uint32_t tops = 0, open = 0;
+  int lost = 0;
   if (have)
 #pragma unroll 4
     for (int i = 0; i < 16; ++i) {
-      const float v = silu_near(bf16_bits_to_f32(gate[i]), bf16_bits_to_f32(up[i]));
+      const float g = bf16_bits_to_f32(gate[i]), u = bf16_bits_to_f32(up[i]), v = silu_near(g, u);
+      lost |= g < kEnd && fabsf(u) >= most * kLost;
       tops |= (uint32_t)(fabsf(v) >= most * (1.0f - 0x1p-19f)) << i;
       open |= (uint32_t)(border(__fmul_rn(v, f)) <= kDoubtful) << i;   // (the kernel's own product)
     }
+  __syncwarp();
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) lost |= __shfl_xor_sync(0xFFFFFFFFu, lost, o);
+  all |= have && lost;
   if (all) tops = open = 0xFFFFu;
   double m = 0x1p-100;
   bool nan = false;
@@ -162,16 +173,21 @@ __global__ void __launch_bounds__(kRowThreads, SWIGLU ? 12 : 8) fp8_rows_kernel(
   float v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  float largest_up = 0.0f;
   if (have) {
-    load16<WIDE>(x + row * (SWIGLU ? 2 * (int64_t)K : K) + c, v);
+    uint32_t w[8];
+    load16<WIDE>(x + row * (SWIGLU ? 2 * (int64_t)K : K) + c, w);
+    unpack16(w, v);
     if (SWIGLU) {
       float up[16];
-      load16<WIDE>(x + row * 2 * (int64_t)K + K + c, up);
+      load16<WIDE>(x + row * 2 * (int64_t)K + K + c, w);
+      unpack16(w, up);
+      largest_up = abs_max16(up);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = silu_near(v[i], up[i]);
     }
   }
-  uint32_t m = abs_max16(v);
+  uint32_t m = __float_as_uint(abs_max16(v));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   const float most = block_max(m), f = __fdiv_rn(kTop, most);
@@ -185,7 +201,8 @@ __global__ void __launch_bounds__(kRowThreads, SWIGLU ? 12 : 8) fp8_rows_kernel(
 #pragma unroll
     for (int i = 0; i < 16; i += 2) doubt = __vimin3_u32(doubt, border(p[i]), border(p[i + 1]));
     const bool all = have && (!(most < INFINITY) || (most < 0x1p-60f && m != 0));
-    if (__any_sync(0xFFFFFFFFu, have && (doubt <= kDoubtful || all)))
+    const bool look = largest_up >= most * kLost;        // an up may outweigh a gate below kEnd
+    if (__any_sync(0xFFFFFFFFu, have && (doubt <= kDoubtful || all || look)))
       settle(x + row * 2 * (int64_t)K + c, x + row * 2 * (int64_t)K + K + c, have, most, f, all, code, scale);
   }
   if (!have) return;
@@ -229,7 +246,9 @@ __global__ void __launch_bounds__(256, 4) fp8_tiles_kernel(const uint16_t* __res
   for (int i = 0; i < 4; ++i)
     if (r0 + 32 * i < N && c < K) {
       float v[16];
-      unpack16(raw[i][0], raw[i][1], v);
+      const uint32_t w8[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                              raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+      unpack16(w8, v);
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], f);
       *reinterpret_cast<uint4*>(q + (base + r0 + 32 * i) * K + c) = e4m3x16(v);

@@ -1,0 +1,84 @@
+"""Edges of the block-scaled E4M3 operators on the GPU: inputs at the ends of their ranges, neighbours of the operands
+in memory, streams, empty calls."""
+import numpy as np
+import pytest
+
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    import nvfp4_weight_only_top_b200 as moe
+    return torch, moe
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------------------------------ SwiGLU
+
+FAR = [-60.0, -61.0, -75.0, -87.0, -87.5, -88.0, -88.5, -89.0, -90.0, -100.0, -130.0, -177.0]
+UPS = [1.0, 1e3, -1e3, 2.0 ** 40, 2.0 ** 99, 1e30, -2.0 ** 106, 3e38]
+
+
+def _swiglu_against_64_bits(gu):
+    """Codes from 2^-6 on are the nearest to the 64-bit products, but for products within 2^-44 of a step of a border
+    between two codes (two computations in 64 bits differ by less); smaller codes are within one subnormal step of
+    2^-9; scales within five steps and two roundings of 32 bits, 6 x 2^-23."""
+    torch, moe = _torch()
+    q, s = moe.moe_nvfp4_fp8_swiglu_quantize(gu)
+    R, I = q.shape
+    h = np.pad(fp8.swiglu(_np(gu)), ((0, 0), (0, -I % 128)))
+    most = np.maximum(np.abs(h).reshape(R, -1, 128).max(2), 2.0 ** -100)
+    p = (h * (448 / most).repeat(128, 1))[:, :I]
+    got, want = _np(q), fp8.e4m3(p)
+    _, e = np.frexp(np.abs(p))
+    steps = np.abs(p) / np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    sure = (np.abs(p) >= 2.0 ** -6) & (np.abs(steps - np.floor(steps) - 0.5) > 2.0 ** -44)
+    assert np.array_equal(got[sure], want[sure])
+    assert (np.abs(got - want)[np.abs(p) < 2.0 ** -6] <= 2.0 ** -9).all()
+    assert (np.abs(_np(s) - most / 448) <= 6 * 2.0 ** -23 * most / 448).all()
+
+
+@pytest.mark.parametrize("I", [128, 144])
+def test_swiglu_far_gates_alone(I):
+    """Blocks of one gate so far below zero that 1 + e^-gate is at the end of f32 or past it, and one up."""
+    torch, _ = _torch()
+    gu = torch.tensor([[g] * I + [u] * I for g in FAR for u in UPS], device="cuda").to(torch.bfloat16)
+    _swiglu_against_64_bits(gu)
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-12, 1e-25])
+def test_swiglu_far_gates_among_ordinary_values(size):
+    """One such value at every place of a block of ordinary ones (small ups make the block small)."""
+    torch, _ = _torch()
+    rng = np.random.default_rng(31)
+    rows, I = len(FAR) * len(UPS), 272
+    g = rng.standard_normal((rows, I)).astype(np.float32)
+    u = (size * rng.standard_normal((rows, I))).astype(np.float32)
+    for r in range(rows):
+        at = (37 * r) % I
+        g[r, at], u[r, at] = FAR[r // len(UPS)], UPS[r % len(UPS)]
+    _swiglu_against_64_bits(torch.from_numpy(np.concatenate([g, u], 1)).cuda().to(torch.bfloat16))
+
+
+def test_swiglu_zero_blocks_beside_far_gates():
+    """Zero gates or zero ups give zero codes and the least scale; a far gate that cannot matter changes nothing."""
+    torch, moe = _torch()
+    gu = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    gu[1, 128:] = 1e30
+    gu[2, :128] = -88.0
+    gu[3, :128] = -300.0
+    gu[3, 128:] = 1e3
+    q, s = moe.moe_nvfp4_fp8_swiglu_quantize(gu)
+    assert (_np(q) == 0).all() and (s == float(np.float32(2.0 ** -100) / np.float32(448))).all()
+    x = torch.randn(4, 256, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    wq, ws = moe.moe_nvfp4_fp8_swiglu_quantize(x)
+    x[:, 5] = -88.0
+    q, s = moe.moe_nvfp4_fp8_swiglu_quantize(x)
+    keep = [i for i in range(128) if i != 5]
+    top = (_np(wq)[:, 5] != 448) & (_np(wq)[:, 5] != -448)      # (where the value replaced was not the largest)
+    assert np.array_equal(_np(q)[top][:, keep], _np(wq)[top][:, keep]) and np.array_equal(_np(s)[top], _np(ws)[top])
