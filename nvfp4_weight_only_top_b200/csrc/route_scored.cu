@@ -236,20 +236,14 @@ __device__ __forceinline__ bool select_fast(const float* __restrict__ row, const
     const float a = fkey_value(x & ~kSlot), b = fkey_value(y & ~kSlot);
     return fabsf(a - b) <= tol + kRel * fmaxf(fabsf(a), fabsf(b));
   };
-  double norm = 0.0;                                     // a softmax's sum in 64 bits, where it is needed
+  double norm = 1.0;                                     // a softmax's sum in 64 bits, where it is needed
   float top = 0.0f, inv_norm = 1.0f, abs_tol = 0x1p-21f;
-  const auto score = [&](float l) -> double {
-    if (r.softmax && norm == 0.0) {                      // (called by whole warps)
-      if (r.bias) {
-        norm = sum64(row + e0, n, top);
+  const auto find_norm = [&]() {                         // (called by whole warps)
+    norm = sum64(row + e0, n, top);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) norm += shfl_xor_f64(norm, o);
-      } else {
-        norm = 1.0;                                      // the order is that of the exponentials
-      }
-    }
-    return score64(l, top, norm, r.softmax);
+    for (int o = 16; o > 0; o >>= 1) norm += shfl_xor_f64(norm, o);
   };
+  const auto score = [&](float l) -> double { return score64(l, top, norm, r.softmax); };
   float v[PER], add[PER];
   bool odd = false;                                      // a NaN, or something far out
 #pragma unroll
@@ -333,6 +327,7 @@ __device__ __forceinline__ bool select_fast(const float* __restrict__ row, const
     if (x - y <= 2.0f * abs_tol + kRel * most) {         // the groups again, in 64 bits
       // A lane's three largest hold its two largest in 64 bits, unless the fourth is near the second.
       if (__any_sync(kFull, n > 3 && key[3] != 0 && near(key[3], key[1], abs_tol))) return false;
+      if (r.softmax) find_norm();
       double c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll 1
       for (int i = 0; i < 3; ++i) {
@@ -395,7 +390,12 @@ __device__ __forceinline__ bool select_fast(const float* __restrict__ row, const
       more = head != 0 && near(head, prev, abs_tol);
     }
     const int e = lane < c ? expert() : 0;
-    l = lane < c ? __ldg(row + e) : 0.0f;
+    l = lane < c ? __ldg(row + e) : top;
+    // Without a bias a softmax's order is that of the exponentials, but where unlike ones divided by the sum are one
+    // double.  That takes two logits within 2^-50 of each other, so one of them, in 32 bits, under 2^-25; or quotients
+    // at the end of 64 bits.
+    const bool by_quotient = r.bias != nullptr || (l != 0.0f && fabsf(l) < 0x1p-25f) || (l - top < -600.0f && l > -INFINITY);
+    if (r.softmax && __any_sync(kFull, by_quotient)) find_norm();
     double value = score(l);
     if (r.bias) value += (double)__ldg(r.bias + e);
     int rank = 0;
