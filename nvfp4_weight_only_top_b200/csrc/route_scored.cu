@@ -414,7 +414,10 @@ __device__ __forceinline__ bool select_fast(const float* __restrict__ row, const
     id = lane < k ? expert() : 0;
     l = lane < k ? __ldg(row + id) : 0.0f;
   }
-  if (__any_sync(kFull, !r.softmax && l < -80.0f && l > -INFINITY)) return false;   // near the end of 32 bits
+  // Weights at the end of 32 bits (and within that of 64): a sigmoid's under 2^-115, a softmax's of an exponent below
+  // -48, whose rounding (2^-24 of it) would also be the larger part of the weight's error.
+  const float least = r.softmax ? top - 48.0f : -80.0f;
+  if (__any_sync(kFull, lane < k && l < least && l > least - 720.0f)) return false;
   float s = 0.0f;
   if (lane < k) s = r.softmax ? expf(l - top) * inv_norm : 1.0f / (1.0f + expf(-l));
   if (r.renormalize) {

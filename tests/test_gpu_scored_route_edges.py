@@ -44,3 +44,24 @@ def test_a_bias_of_zeros_changes_nothing(T, groups, top_groups, group_top):
         # weights of two ways: two exponentials (2 steps each), a sum, a division, a tree of 5 additions and a division
         # in 32 bits on one side and 64 bits rounded once on the other, under 16 half steps of 2^-24
         assert (np.abs(a["w"] - b["w"]) <= 16 * 2.0 ** -24 * np.abs(b["w"])).all()
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_small_weights(score, renormalize):
+    """Chosen experts whose scores are at the end of f32, with a scale that takes them back into its range.
+
+    Error: 16 half steps of 2^-24 (two exponentials, a sum, a division, a tree of additions, a division, the scale),
+    and the rounding of an exponent's argument, up to 48 x 2^-24 for a softmax's; 2^-149 where the weight is subnormal."""
+    rng = np.random.default_rng(17)
+    T, E, k = 40, 32, 6
+    far = np.exp2(rng.uniform(3, 9.4, (T, 1)))                   # 8 .. 676 below the largest
+    lg = -(far + 8 * rng.random((T, E))).astype(np.float32)
+    if score == "softmax":
+        lg[:, 7] = rng.standard_normal(T)
+        lg += 3 * rng.standard_normal((T, 1)).astype(np.float32)
+    lg = lg.astype(np.float32)
+    for scale in (1.0, 2.0 ** 60, 2.0 ** 120):
+        w = _route(lg, k, score=score, renormalize=renormalize, scale=scale)["w"]
+        ids, want = scored.route_scored(lg, k, score=score, renormalize=renormalize, scale=scale)
+        assert (np.abs(w - want) <= 64 * 2.0 ** -24 * want + 2.0 ** -149).all(), scale
