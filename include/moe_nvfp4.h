@@ -276,6 +276,7 @@ int moe_nvfp4_forward_scored(const void* x_dev, const float* logits_dev, int64_t
  * moe_nvfp4_fp8_quantize         x_dev [T, K] BF16.  inv_dev NULL and k = 1: row t to row t.  Else
  *     inv_dev [T*k] int32 and 1 <= k <= 32: row t to the k rows inv[t*k + j] of q_dev [T*k, K] --
  *     with a router's inv, the routed rows in expert order.  An entry outside [0, T*k) is skipped.
+ *     With T = 0 inv_dev may be NULL for every k.
  * moe_nvfp4_fp8_swiglu_quantize  gu_dev [R, 2 I] BF16, gate in columns 0 .. I-1 and up behind it:
  *     q_dev [R, I], scales_dev [R, ceil(I/128)] of silu(gate) * up = gate / (1 + exp(-gate)) * up.
  *     Codes from 2^-6 on are those of 64 bits; smaller ones and the scales are formed in f32.

@@ -57,7 +57,7 @@ int moe_nvfp4_fp8_quantize(const void* x_dev, int64_t T, int32_t K, const int32_
   int rc = check_rows(T, "T is negative");
   if (rc || (rc = check_width(K, "K"))) return rc;
   if (k < 1 || k > 32) return bad("k outside 1..32", k);
-  if (!inv_dev && k != 1) return bad("k must be 1 without inv", k);
+  if (T > 0 && !inv_dev && k != 1) return bad("k must be 1 without inv", k);   // (an empty inv has no address)
   if (T * k >= (int64_t)1 << 26) return moe::api_fail(MOE_NVFP4_ERR_UNSUPPORTED, "too many rows (limit 2^26)");
   int dev, sms;
   if ((rc = moe::api_device(&dev, &sms))) return rc;

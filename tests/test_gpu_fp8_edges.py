@@ -82,3 +82,22 @@ def test_swiglu_zero_blocks_beside_far_gates():
     keep = [i for i in range(128) if i != 5]
     top = (_np(wq)[:, 5] != 448) & (_np(wq)[:, 5] != -448)      # (where the value replaced was not the largest)
     assert np.array_equal(_np(q)[top][:, keep], _np(wq)[top][:, keep]) and np.array_equal(_np(s)[top], _np(ws)[top])
+
+
+# ------------------------------------------------------------------------------------------ no rows
+
+def test_an_e4m3_layer_of_no_tokens():
+    torch, moe = _torch()
+    E, k, H, I = 8, 4, 256, 128
+    bf = torch.bfloat16
+    bgu, sgu = moe.moe_nvfp4_fp8_quantize_weights(torch.ones(E, 2 * I, H, dtype=bf, device="cuda"))
+    bd, sd = moe.moe_nvfp4_fp8_quantize_weights(torch.ones(E, H, I, dtype=bf, device="cuda"))
+    r = moe.moe_nvfp4_route_scored(torch.empty(0, E, device="cuda"), moe.make_router(), k)
+    q, s = moe.moe_nvfp4_fp8_quantize(torch.empty(0, H, dtype=bf, device="cuda"), inv=r["inv"], k=k)
+    gu = moe.moe_nvfp4_fp8_matmul(q, s, bgu, sgu, r["offsets"])
+    h, hs = moe.moe_nvfp4_fp8_swiglu_quantize(gu)
+    y = moe.moe_nvfp4_fp8_matmul(h, hs, bd, sd, r["offsets"], out_dtype=torch.float32)
+    out = moe.moe_nvfp4_combine(y, r["w"], r["inv"], k)
+    torch.cuda.synchronize()
+    assert q.shape == (0, H) and s.shape == (0, 2) and gu.shape == (0, 2 * I) and out.shape == (0, H)
+    assert moe.moe_nvfp4_device_status() == 0
