@@ -3,6 +3,11 @@
 Thin Python binding over the C ABI of libmoe_nvfp4.so (include/moe_nvfp4.h).  The functions
 carry the C entry points' names and only marshal arguments: tensors are PyTorch CUDA tensors
 (device memory and streams), every step of the layer runs in the library's kernels.
+
+A call runs on `stream`, or on the current stream where that is None, and makes the outputs that it is
+not given on the same stream: their memory is that stream's, and comes back to it when they are freed.
+The caller orders the stream behind the inputs, other streams behind the call, and calls
+Tensor.record_stream for a stream that uses an output past its last reference, as with any PyTorch call.
 """
 from __future__ import annotations
 
@@ -102,6 +107,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _made_on(stream, make):
+    """make(), its tensors allocated on `stream` (None: the current one).  Made on the current stream instead, they
+    could be memory that this stream's work still reads, or be given out again while `stream` still writes them."""
+    if stream is None:
+        return make()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def make_bank(base_ptr: int, num_experts: int, hidden: int, intermediate: int, record_stride: int,
               codes_off, scales_off, global_off, global_mode: int = 0) -> Bank:
     """moe_nvfp4_bank for E records at device address base_ptr."""
@@ -118,7 +135,7 @@ def moe_nvfp4_forward(x, logits, bank: Bank, k: int, out=None, stream=None):
     """out [T, H] bf16 = MoE(x [T, H] bf16, logits [T, E] f32) on the current device."""
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = torch.empty_like(x)
+        out = _made_on(stream, lambda: torch.empty_like(x))
     T = _layer_args(x, logits, bank, out)
     _check(lib().moe_nvfp4_forward(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
                                    _stream(stream)))
@@ -130,7 +147,7 @@ def moe_nvfp4_forward_ex(x, logits, bank: Bank, k: int, out=None, x_next=None, w
     """As moe_nvfp4_forward, with optional residual output, caller workspace and path."""
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = torch.empty_like(x)
+        out = _made_on(stream, lambda: torch.empty_like(x))
     T = _layer_args(x, logits, bank, out, x_next, workspace)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().moe_nvfp4_forward_ex(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
@@ -146,7 +163,7 @@ def moe_nvfp4_forward_w4a4(x, logits, bank: Bank, act_scales, k: int, out=None, 
     "h_scales" [T*k, I/16] u8 (device tensors) to outputs filled in slot order."""
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = torch.empty_like(x)
+        out = _made_on(stream, lambda: torch.empty_like(x))
     H, I = bank.hidden, bank.intermediate
     for name in (taps or {}):
         if name not in ("x_codes", "x_scales", "h", "h_codes", "h_scales"):
@@ -179,7 +196,7 @@ def moe_nvfp4_forward_noalloc(x, logits, bank: Bank, k: int, out=None, stream=No
     """
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = torch.empty_like(x)
+        out = _made_on(stream, lambda: torch.empty_like(x))
     T = _layer_args(x, logits, bank, out)
     _check(lib().moe_nvfp4_forward_noalloc(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
                                            _stream(stream)))
@@ -218,12 +235,12 @@ def moe_nvfp4_route(logits, k: int, stream=None) -> dict:
     T, E = (int(v) for v in logits.shape)
     _need("logits", logits, torch.float32, (T, E))
     dev = logits.device
-    r = dict(ids=torch.empty((T, k), dtype=torch.int32, device=dev),
-             w=torch.empty((T, k), dtype=torch.float32, device=dev),
-             counts=torch.empty(E, dtype=torch.int32, device=dev),
-             offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-             perm=torch.empty(T * k, dtype=torch.int32, device=dev),
-             inv=torch.empty(T * k, dtype=torch.int32, device=dev))
+    r = _made_on(stream, lambda: dict(ids=torch.empty((T, k), dtype=torch.int32, device=dev),
+                                      w=torch.empty((T, k), dtype=torch.float32, device=dev),
+                                      counts=torch.empty(E, dtype=torch.int32, device=dev),
+                                      offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                                      perm=torch.empty(T * k, dtype=torch.int32, device=dev),
+                                      inv=torch.empty(T * k, dtype=torch.int32, device=dev)))
     _check(lib().moe_nvfp4_route(_ptr(logits), T, E, k, _ptr(r["ids"]), _ptr(r["w"]), _ptr(r["counts"]),
                                  _ptr(r["offsets"]), _ptr(r["perm"]), _ptr(r["inv"]), _stream(stream)))
     return r
@@ -277,9 +294,8 @@ def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
         raise ValueError(f"k = {k} outside 1..min(E={E}, 32)")
     R = T * k
     # three allocations for the six outputs (an allocation, or a view, costs the host as much as a small launch)
-    w = logits.new_empty((T, k))
-    ids = logits.new_empty((T, k), dtype=torch.int32)
-    buf = logits.new_empty(2 * R + 2 * E + 1, dtype=torch.int32)
+    w, ids, buf = _made_on(stream, lambda: (logits.new_empty((T, k)), logits.new_empty((T, k), dtype=torch.int32),
+                                            logits.new_empty(2 * R + 2 * E + 1, dtype=torch.int32)))
     perm, inv, counts, offsets = buf.split_with_sizes((R, R, E, E + 1))
     at = buf.data_ptr()
     _check(lib().moe_nvfp4_route_scored(logits.data_ptr(), T, E, ctypes.byref(router), k, ids.data_ptr(), w.data_ptr(),
@@ -292,7 +308,7 @@ def moe_nvfp4_forward_scored(x, logits, bank: Bank, router: Router, k: int, out=
     """moe_nvfp4_forward_ex with the scored router."""
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = torch.empty_like(x)
+        out = _made_on(stream, lambda: torch.empty_like(x))
     T = _layer_args(x, logits, bank, out, x_next, workspace)
     _router_bias(router, bank.num_experts)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -301,15 +317,18 @@ def moe_nvfp4_forward_scored(x, logits, bank: Bank, router: Router, k: int, out=
     return out
 
 
-def _fp8_out(x, q, scales, shape, scale_shape, dev):
+def _fp8_out(x, q, scales, shape, scale_shape, dev, stream):
     """The outputs of a quantizer: made here, or the caller's, checked."""
     import torch
+    if q is None and scales is None:
+        return _made_on(stream, lambda: (x.new_empty(shape, dtype=torch.float8_e4m3fn),
+                                         x.new_empty(scale_shape, dtype=torch.float32)))
     if q is None:
-        q = x.new_empty(shape, dtype=torch.float8_e4m3fn)
+        q = _made_on(stream, lambda: x.new_empty(shape, dtype=torch.float8_e4m3fn))
     else:
         _fits("q", q, torch.float8_e4m3fn, shape, dev)
     if scales is None:
-        scales = x.new_empty(scale_shape, dtype=torch.float32)
+        scales = _made_on(stream, lambda: x.new_empty(scale_shape, dtype=torch.float32))
     else:
         _fits("scales", scales, torch.float32, scale_shape, dev)
     return q, scales
@@ -335,7 +354,7 @@ def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=
     dev = _fp8_in("x", x)
     if inv is not None:
         _fits("inv", inv, torch.int32, (T * k,), dev)
-    q, scales = _fp8_out(x, q, scales, (T * k, K), (T * k, (K + 127) // 128), dev)
+    q, scales = _fp8_out(x, q, scales, (T * k, K), (T * k, (K + 127) // 128), dev, stream)
     _check(lib().moe_nvfp4_fp8_quantize(x.data_ptr(), T, K, _addr(inv), k, q.data_ptr(), scales.data_ptr(),
                                         _raw_stream(stream, dev)))
     return q, scales
@@ -349,7 +368,7 @@ def moe_nvfp4_fp8_swiglu_quantize(gu, q=None, scales=None, stream=None):
     R, I = gu.shape
     I //= 2
     dev = _fp8_in("gu", gu)
-    q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev)
+    q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev, stream)
     _check(lib().moe_nvfp4_fp8_swiglu_quantize(gu.data_ptr(), R, I, q.data_ptr(), scales.data_ptr(),
                                                _raw_stream(stream, dev)))
     return q, scales
@@ -364,7 +383,8 @@ def moe_nvfp4_fp8_quantize_weights(w, q=None, scales=None, stream=None):
     shape = tuple(w.shape)
     n, N, K = (1,) * (3 - w.dim()) + shape
     dev = _fp8_in("w", w)
-    q, scales = _fp8_out(w, q, scales, shape, shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dev)
+    tiles = shape[:-2] + ((N + 127) // 128, (K + 127) // 128)
+    q, scales = _fp8_out(w, q, scales, shape, tiles, dev, stream)
     _check(lib().moe_nvfp4_fp8_quantize_weights(w.data_ptr(), n, N, K, q.data_ptr(), scales.data_ptr(),
                                                 _raw_stream(stream, dev)))
     return q, scales
@@ -403,7 +423,7 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
     _fits("a_scales", a_scales, torch.float32, (M, kb), dev)
     _fits("b_scales", b_scales, torch.float32, tiles, dev)
     if out is None:
-        out = a.new_empty((M, N), dtype=torch.float32 if f32 else torch.bfloat16)
+        out = _made_on(stream, lambda: a.new_empty((M, N), dtype=torch.float32 if f32 else torch.bfloat16))
     else:
         _fits("out", out, out.dtype, (M, N), dev)
     if offsets is not None:
@@ -424,7 +444,7 @@ def moe_nvfp4_experts(x_rows, expert_ids, bank: Bank, y_rows=None, workspace=Non
         raise ValueError("x_rows must be a 2-D torch tensor [R, H]")
     R = int(x_rows.shape[0])
     if y_rows is None:
-        y_rows = torch.empty((R, bank.hidden), dtype=torch.float32, device=x_rows.device)
+        y_rows = _made_on(stream, lambda: torch.empty((R, bank.hidden), dtype=torch.float32, device=x_rows.device))
     need = [("x_rows", x_rows, torch.bfloat16, (R, bank.hidden)), ("expert_ids", expert_ids, torch.int32, (R,)),
             ("y_rows", y_rows, torch.float32, (R, bank.hidden))]
     if workspace is not None:
@@ -451,7 +471,7 @@ def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
         raise ValueError("x must be a 2-D torch tensor [T, H]")
     T, H = (int(v) for v in x.shape)
     if rows is None:
-        rows = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
+        rows = _made_on(stream, lambda: torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device))
     need = [("x", x, torch.bfloat16, (T, H)), ("perm", perm, torch.int32, (T * k,)),
             ("rows", rows, torch.bfloat16, (T * k, H))]
     for args in need:
@@ -472,7 +492,7 @@ def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=N
         raise ValueError("y must be a 2-D torch tensor [T*k, H]")
     H = int(y.shape[1])
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+        out = _made_on(stream, lambda: torch.empty((T, H), dtype=torch.bfloat16, device=y.device))
     need = [("y", y, torch.float32, (T * k, H)), ("w", w, torch.float32, (T, k)), ("inv", inv, torch.int32, (T * k,)),
             ("out", out, torch.bfloat16, (T, H))]
     if x_next is not None:
@@ -494,8 +514,9 @@ def moe_nvfp4_ep_plan(counts_all, rank: int, recv_rows: int, layout: int = _abi.
         raise ValueError("counts_all must be a 2-D torch tensor [G, E]")
     G, E = (int(v) for v in counts_all.shape)
     _need("counts_all", counts_all, torch.int32, (G, E))
-    dst_off = torch.empty(E, dtype=torch.int32, device=counts_all.device)
-    recv_ids = torch.empty(max(int(recv_rows), 1), dtype=torch.int32, device=counts_all.device)
+    dev = counts_all.device
+    dst_off, recv_ids = _made_on(stream, lambda: (torch.empty(E, dtype=torch.int32, device=dev),
+                                                  torch.empty(max(int(recv_rows), 1), dtype=torch.int32, device=dev)))
     _check(lib().moe_nvfp4_ep_plan(_ptr(counts_all), G, E, rank, layout, _ptr(dst_off), _ptr(recv_ids),
                                    int(recv_rows), _stream(stream)))
     return dst_off, recv_ids[:int(recv_rows)]
@@ -539,7 +560,7 @@ def moe_nvfp4_ep_combine(route: dict, dst_off, recv_y_ptrs, hidden: int, capacit
     H = int(hidden)
     G = len(recv_y_ptrs)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dst_off.device)
+        out = _made_on(stream, lambda: torch.empty((T, H), dtype=torch.bfloat16, device=dst_off.device))
     need = [("dst_off", dst_off, torch.int32, (E,)), ("out", out, torch.bfloat16, (T, H))] + _route_need(route, T, k, E)
     if x_next is not None:
         need += [("x", x, torch.bfloat16, (T, H)), ("x_next", x_next, torch.bfloat16, (T, H))]
@@ -623,7 +644,7 @@ def encode_bank(gate, up, down, global_mode: int = 0, stream=None):
     if tuple(up.shape) != (E, I, H) or tuple(down.shape) != (E, H, I):
         raise ValueError("gate and up must be [E, I, H] and down [E, H, I]")
     lay = record_layout(H, I)
-    buf = torch.zeros(E * lay["record_stride"], dtype=torch.uint8, device=gate.device)
+    buf = _made_on(stream, lambda: torch.zeros(E * lay["record_stride"], dtype=torch.uint8, device=gate.device))
     for p, w in enumerate((gate, up, down)):
         moe_nvfp4_encode(w, buf, lay["record_stride"], lay["codes_off"][p], lay["scales_off"][p],
                          lay["global_off"][p], global_mode, stream)
@@ -680,7 +701,7 @@ class Pack:
         """A whole layer resident on the current device: (uint8 tensor, moe_nvfp4_bank)."""
         import torch
         i = self.info
-        buf = torch.empty(i["experts"] * i["record_stride"], dtype=torch.uint8, device="cuda")
+        buf = _made_on(stream, lambda: torch.empty(i["experts"] * i["record_stride"], dtype=torch.uint8, device="cuda"))
         self.load(layer, buf, verify=verify, stream=stream)
         bank = make_bank(buf.data_ptr(), i["experts"], i["hidden"], i["intermediate"], i["record_stride"],
                          i["codes_off"], i["scales_off"], i["global_off"], i["global_mode"])
@@ -704,7 +725,7 @@ class Rows:
         import torch
         i = self.pack.info
         if out is None and isinstance(x, torch.Tensor):
-            out = torch.empty_like(x)
+            out = _made_on(stream, lambda: torch.empty_like(x))
         bank = Bank()
         bank.hidden, bank.num_experts = i["hidden"], i["experts"]
         T = _layer_args(x, logits, bank, out)
