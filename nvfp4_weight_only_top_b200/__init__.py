@@ -98,25 +98,23 @@ def _fits(name: str, t, dtype, shape, dev: int) -> None:
         _need(name, t, dtype, shape)
 
 
-def _raw_stream(stream, dev: int) -> int:
+def _raw_stream(dev: int) -> int:
+    """The current stream of the device."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _made_on(stream, make):
-    """make(), its tensors allocated on `stream` (None: the current one).  Made on the current stream instead, they
-    could be memory that this stream's work still reads, or be given out again while `stream` still writes them."""
-    if stream is None:
-        return make()
+def _on(stream):
+    """The context of a call with a stream: it runs, and allocates its outputs, on that one.  (Made on the stream that is
+    current, they could be memory that its work still reads, or be given out again while `stream` still writes them.)"""
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
-        return make()
+    return torch.cuda.stream(stream)
 
 
 def make_bank(base_ptr: int, num_experts: int, hidden: int, intermediate: int, record_stride: int,
@@ -133,9 +131,12 @@ def make_bank(base_ptr: int, num_experts: int, hidden: int, intermediate: int, r
 
 def moe_nvfp4_forward(x, logits, bank: Bank, k: int, out=None, stream=None):
     """out [T, H] bf16 = MoE(x [T, H] bf16, logits [T, E] f32) on the current device."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_forward(x, logits, bank, k, out)
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = _made_on(stream, lambda: torch.empty_like(x))
+        out = torch.empty_like(x)
     T = _layer_args(x, logits, bank, out)
     _check(lib().moe_nvfp4_forward(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
                                    _stream(stream)))
@@ -145,9 +146,12 @@ def moe_nvfp4_forward(x, logits, bank: Bank, k: int, out=None, stream=None):
 def moe_nvfp4_forward_ex(x, logits, bank: Bank, k: int, out=None, x_next=None, workspace=None,
                          path: int = PATH_AUTO, stream=None):
     """As moe_nvfp4_forward, with optional residual output, caller workspace and path."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_forward_ex(x, logits, bank, k, out, x_next, workspace, path)
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = _made_on(stream, lambda: torch.empty_like(x))
+        out = torch.empty_like(x)
     T = _layer_args(x, logits, bank, out, x_next, workspace)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().moe_nvfp4_forward_ex(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
@@ -161,9 +165,12 @@ def moe_nvfp4_forward_w4a4(x, logits, bank: Bank, act_scales, k: int, out=None, 
     expert's input multipliers of gate/up and of down.  taps, if given, maps any of "x_codes"
     [T*k, H/2] u8, "x_scales" [T*k, H/16] u8, "h" [T*k, I] f32, "h_codes" [T*k, I/2] u8 and
     "h_scales" [T*k, I/16] u8 (device tensors) to outputs filled in slot order."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_forward_w4a4(x, logits, bank, act_scales, k, out, x_next, workspace, taps)
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = _made_on(stream, lambda: torch.empty_like(x))
+        out = torch.empty_like(x)
     H, I = bank.hidden, bank.intermediate
     for name in (taps or {}):
         if name not in ("x_codes", "x_scales", "h", "h_codes", "h_scales"):
@@ -194,9 +201,12 @@ def moe_nvfp4_forward_noalloc(x, logits, bank: Bank, k: int, out=None, stream=No
     For callers that cannot allocate device memory during a call; `out` may be passed in so
     that the call itself allocates nothing on the Python side either.
     """
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_forward_noalloc(x, logits, bank, k, out)
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = _made_on(stream, lambda: torch.empty_like(x))
+        out = torch.empty_like(x)
     T = _layer_args(x, logits, bank, out)
     _check(lib().moe_nvfp4_forward_noalloc(_ptr(x), _ptr(logits), T, ctypes.byref(bank), k, _ptr(out),
                                            _stream(stream)))
@@ -229,18 +239,21 @@ def moe_nvfp4_forward_host(x_host: np.ndarray, logits_host: np.ndarray, bank: Ba
 
 def moe_nvfp4_route(logits, k: int, stream=None) -> dict:
     """Routing only: ids, w, counts, offsets, perm, inv (int32 / f32 CUDA tensors)."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_route(logits, k)
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
     T, E = (int(v) for v in logits.shape)
     _need("logits", logits, torch.float32, (T, E))
     dev = logits.device
-    r = _made_on(stream, lambda: dict(ids=torch.empty((T, k), dtype=torch.int32, device=dev),
-                                      w=torch.empty((T, k), dtype=torch.float32, device=dev),
-                                      counts=torch.empty(E, dtype=torch.int32, device=dev),
-                                      offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                                      perm=torch.empty(T * k, dtype=torch.int32, device=dev),
-                                      inv=torch.empty(T * k, dtype=torch.int32, device=dev)))
+    r = dict(ids=torch.empty((T, k), dtype=torch.int32, device=dev),
+             w=torch.empty((T, k), dtype=torch.float32, device=dev),
+             counts=torch.empty(E, dtype=torch.int32, device=dev),
+             offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+             perm=torch.empty(T * k, dtype=torch.int32, device=dev),
+             inv=torch.empty(T * k, dtype=torch.int32, device=dev))
     _check(lib().moe_nvfp4_route(_ptr(logits), T, E, k, _ptr(r["ids"]), _ptr(r["w"]), _ptr(r["counts"]),
                                  _ptr(r["offsets"]), _ptr(r["perm"]), _ptr(r["inv"]), _stream(stream)))
     return r
@@ -281,6 +294,9 @@ def _router_bias(router: Router, E: int) -> None:
 
 def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
     """Scored routing (include/moe_nvfp4.h): ids, w, counts, offsets, perm, inv, as moe_nvfp4_route."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_route_scored(logits, router, k)
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
@@ -294,21 +310,25 @@ def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
         raise ValueError(f"k = {k} outside 1..min(E={E}, 32)")
     R = T * k
     # three allocations for the six outputs (an allocation, or a view, costs the host as much as a small launch)
-    w, ids, buf = _made_on(stream, lambda: (logits.new_empty((T, k)), logits.new_empty((T, k), dtype=torch.int32),
-                                            logits.new_empty(2 * R + 2 * E + 1, dtype=torch.int32)))
+    w = logits.new_empty((T, k))
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    buf = logits.new_empty(2 * R + 2 * E + 1, dtype=torch.int32)
     perm, inv, counts, offsets = buf.split_with_sizes((R, R, E, E + 1))
     at = buf.data_ptr()
     _check(lib().moe_nvfp4_route_scored(logits.data_ptr(), T, E, ctypes.byref(router), k, ids.data_ptr(), w.data_ptr(),
-                                        at + 8 * R, at + 8 * R + 4 * E, at, at + 4 * R, _raw_stream(stream, dev)))
+                                        at + 8 * R, at + 8 * R + 4 * E, at, at + 4 * R, _raw_stream(dev)))
     return dict(ids=ids, w=w, counts=counts, offsets=offsets, perm=perm, inv=inv)
 
 
 def moe_nvfp4_forward_scored(x, logits, bank: Bank, router: Router, k: int, out=None, x_next=None, workspace=None,
                              path: int = PATH_AUTO, stream=None):
     """moe_nvfp4_forward_ex with the scored router."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_forward_scored(x, logits, bank, router, k, out, x_next, workspace, path)
     import torch
     if out is None and isinstance(x, torch.Tensor):
-        out = _made_on(stream, lambda: torch.empty_like(x))
+        out = torch.empty_like(x)
     T = _layer_args(x, logits, bank, out, x_next, workspace)
     _router_bias(router, bank.num_experts)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -317,18 +337,15 @@ def moe_nvfp4_forward_scored(x, logits, bank: Bank, router: Router, k: int, out=
     return out
 
 
-def _fp8_out(x, q, scales, shape, scale_shape, dev, stream):
+def _fp8_out(x, q, scales, shape, scale_shape, dev):
     """The outputs of a quantizer: made here, or the caller's, checked."""
     import torch
-    if q is None and scales is None:
-        return _made_on(stream, lambda: (x.new_empty(shape, dtype=torch.float8_e4m3fn),
-                                         x.new_empty(scale_shape, dtype=torch.float32)))
     if q is None:
-        q = _made_on(stream, lambda: x.new_empty(shape, dtype=torch.float8_e4m3fn))
+        q = x.new_empty(shape, dtype=torch.float8_e4m3fn)
     else:
         _fits("q", q, torch.float8_e4m3fn, shape, dev)
     if scales is None:
-        scales = _made_on(stream, lambda: x.new_empty(scale_shape, dtype=torch.float32))
+        scales = x.new_empty(scale_shape, dtype=torch.float32)
     else:
         _fits("scales", scales, torch.float32, scale_shape, dev)
     return q, scales
@@ -347,6 +364,9 @@ def _fp8_in(name: str, x):
 def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=None):
     """x [T, K] bf16 to E4M3 codes q [T*k, K] and f32 scales [T*k, ceil(K/128)], one scale per 128
     inputs.  inv [T*k] int32 (a router's): row t goes to the rows inv[t*k + j], the expert order."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_fp8_quantize(x, inv, k, q, scales)
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, K]")
@@ -354,39 +374,44 @@ def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=
     dev = _fp8_in("x", x)
     if inv is not None:
         _fits("inv", inv, torch.int32, (T * k,), dev)
-    q, scales = _fp8_out(x, q, scales, (T * k, K), (T * k, (K + 127) // 128), dev, stream)
+    q, scales = _fp8_out(x, q, scales, (T * k, K), (T * k, (K + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_quantize(x.data_ptr(), T, K, _addr(inv), k, q.data_ptr(), scales.data_ptr(),
-                                        _raw_stream(stream, dev)))
+                                        _raw_stream(dev)))
     return q, scales
 
 
 def moe_nvfp4_fp8_swiglu_quantize(gu, q=None, scales=None, stream=None):
     """silu(gate) * up of gu [R, 2 I] bf16 (gate first), quantized: q [R, I] and scales [R, ceil(I/128)]."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_fp8_swiglu_quantize(gu, q, scales)
     import torch
     if not isinstance(gu, torch.Tensor) or gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must be a 2-D torch tensor [R, 2 I]")
     R, I = gu.shape
     I //= 2
     dev = _fp8_in("gu", gu)
-    q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev, stream)
+    q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_swiglu_quantize(gu.data_ptr(), R, I, q.data_ptr(), scales.data_ptr(),
-                                               _raw_stream(stream, dev)))
+                                               _raw_stream(dev)))
     return q, scales
 
 
 def moe_nvfp4_fp8_quantize_weights(w, q=None, scales=None, stream=None):
     """w [n, N, K] (or [N, K]) bf16 to E4M3 codes and f32 scales [n, ceil(N/128), ceil(K/128)], one per
     128 x 128 tile."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_fp8_quantize_weights(w, q, scales)
     import torch
     if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
         raise ValueError("w must be a torch tensor [n, N, K] or [N, K]")
     shape = tuple(w.shape)
     n, N, K = (1,) * (3 - w.dim()) + shape
     dev = _fp8_in("w", w)
-    tiles = shape[:-2] + ((N + 127) // 128, (K + 127) // 128)
-    q, scales = _fp8_out(w, q, scales, shape, tiles, dev, stream)
+    q, scales = _fp8_out(w, q, scales, shape, shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_quantize_weights(w.data_ptr(), n, N, K, q.data_ptr(), scales.data_ptr(),
-                                                _raw_stream(stream, dev)))
+                                                _raw_stream(dev)))
     return q, scales
 
 
@@ -394,6 +419,9 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
     """out [M, N] = the block-scaled products of a [M, K] with b [E, N, K] (or [N, K]), E4M3 both: rows
     offsets[e] .. offsets[e+1]-1 with b[e].  offsets [E+1] int32, or None for one weight and all rows.
     out_dtype torch.bfloat16 (the default) or torch.float32."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets, out, out_dtype)
     import torch
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a must be a 2-D torch tensor [M, K]")
@@ -423,14 +451,14 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
     _fits("a_scales", a_scales, torch.float32, (M, kb), dev)
     _fits("b_scales", b_scales, torch.float32, tiles, dev)
     if out is None:
-        out = _made_on(stream, lambda: a.new_empty((M, N), dtype=torch.float32 if f32 else torch.bfloat16))
+        out = a.new_empty((M, N), dtype=torch.float32 if f32 else torch.bfloat16)
     else:
         _fits("out", out, out.dtype, (M, N), dev)
     if offsets is not None:
         _fits("offsets", offsets, torch.int32, (E + 1,), dev)
     _check(lib().moe_nvfp4_fp8_matmul(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E, N, K,
                                       _addr(offsets), out.data_ptr(), _abi.FP8_OUT_F32 if f32 else _abi.FP8_OUT_BF16,
-                                      _raw_stream(stream, dev)))
+                                      _raw_stream(dev)))
     return out
 
 
@@ -439,12 +467,15 @@ def moe_nvfp4_experts(x_rows, expert_ids, bank: Bank, y_rows=None, workspace=Non
     """y_rows [R, H] f32 = expert expert_ids[r] applied to x_rows[r] (bf16 [R, H]); ids outside
     [0, E) are padding rows (zero output).  sorted_ids: the caller knows the ids are
     non-decreasing and all valid (MOE_NVFP4_EXPERTS_SORTED)."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_experts(x_rows, expert_ids, bank, y_rows, workspace, path, sorted_ids)
     import torch
     if not isinstance(x_rows, torch.Tensor) or x_rows.dim() != 2:
         raise ValueError("x_rows must be a 2-D torch tensor [R, H]")
     R = int(x_rows.shape[0])
     if y_rows is None:
-        y_rows = _made_on(stream, lambda: torch.empty((R, bank.hidden), dtype=torch.float32, device=x_rows.device))
+        y_rows = torch.empty((R, bank.hidden), dtype=torch.float32, device=x_rows.device)
     need = [("x_rows", x_rows, torch.bfloat16, (R, bank.hidden)), ("expert_ids", expert_ids, torch.int32, (R,)),
             ("y_rows", y_rows, torch.float32, (R, bank.hidden))]
     if workspace is not None:
@@ -466,12 +497,15 @@ def moe_nvfp4_experts_workspace_bytes(R: int, E: int, H: int, I: int, path: int 
 
 def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
     """rows [T*k, H] bf16 = x[perm[p] // k]: the routed rows in expert order."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_gather_rows(x, perm, k, rows)
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, H]")
     T, H = (int(v) for v in x.shape)
     if rows is None:
-        rows = _made_on(stream, lambda: torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device))
+        rows = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
     need = [("x", x, torch.bfloat16, (T, H)), ("perm", perm, torch.int32, (T * k,)),
             ("rows", rows, torch.bfloat16, (T * k, H))]
     for args in need:
@@ -484,6 +518,9 @@ def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
 
 def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=None):
     """out [T, H] bf16 = bf16(sum_j w[t, j] * y[inv[t*k+j]]), y f32 [T*k, H] in expert order."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_combine(y, w, inv, k, out, x, x_next)
     import torch
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a 2-D torch tensor [T, k]")
@@ -492,7 +529,7 @@ def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=N
         raise ValueError("y must be a 2-D torch tensor [T*k, H]")
     H = int(y.shape[1])
     if out is None:
-        out = _made_on(stream, lambda: torch.empty((T, H), dtype=torch.bfloat16, device=y.device))
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
     need = [("y", y, torch.float32, (T * k, H)), ("w", w, torch.float32, (T, k)), ("inv", inv, torch.int32, (T * k,)),
             ("out", out, torch.bfloat16, (T, H))]
     if x_next is not None:
@@ -509,14 +546,16 @@ def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=N
 def moe_nvfp4_ep_plan(counts_all, rank: int, recv_rows: int, layout: int = _abi.EP_EXPERT_MAJOR, stream=None):
     """From counts_all [G, E] int32 (row s = rank s's routed rows per expert): dst_off [E] and
     recv_ids [recv_rows] (int32 CUDA tensors), as include/moe_nvfp4.h describes."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_ep_plan(counts_all, rank, recv_rows, layout)
     import torch
     if not isinstance(counts_all, torch.Tensor) or counts_all.dim() != 2:
         raise ValueError("counts_all must be a 2-D torch tensor [G, E]")
     G, E = (int(v) for v in counts_all.shape)
     _need("counts_all", counts_all, torch.int32, (G, E))
-    dev = counts_all.device
-    dst_off, recv_ids = _made_on(stream, lambda: (torch.empty(E, dtype=torch.int32, device=dev),
-                                                  torch.empty(max(int(recv_rows), 1), dtype=torch.int32, device=dev)))
+    dst_off = torch.empty(E, dtype=torch.int32, device=counts_all.device)
+    recv_ids = torch.empty(max(int(recv_rows), 1), dtype=torch.int32, device=counts_all.device)
     _check(lib().moe_nvfp4_ep_plan(_ptr(counts_all), G, E, rank, layout, _ptr(dst_off), _ptr(recv_ids),
                                    int(recv_rows), _stream(stream)))
     return dst_off, recv_ids[:int(recv_rows)]
@@ -554,13 +593,16 @@ def moe_nvfp4_ep_combine(route: dict, dst_off, recv_y_ptrs, hidden: int, capacit
     """out [T, H] bf16 = the layer's combine of the routed rows' expert outputs, read from their
     owners' f32 output buffers (recv_y_ptrs: G device addresses valid in this process, each of
     capacity_rows rows)."""
+    if stream is not None:
+        with _on(stream):
+            return moe_nvfp4_ep_combine(route, dst_off, recv_y_ptrs, hidden, capacity_rows, out, x, x_next)
     import torch
     T, k = (int(v) for v in route["ids"].shape)
     E = int(dst_off.shape[0])
     H = int(hidden)
     G = len(recv_y_ptrs)
     if out is None:
-        out = _made_on(stream, lambda: torch.empty((T, H), dtype=torch.bfloat16, device=dst_off.device))
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dst_off.device)
     need = [("dst_off", dst_off, torch.int32, (E,)), ("out", out, torch.bfloat16, (T, H))] + _route_need(route, T, k, E)
     if x_next is not None:
         need += [("x", x, torch.bfloat16, (T, H)), ("x_next", x_next, torch.bfloat16, (T, H))]
@@ -639,12 +681,15 @@ def record_layout(hidden: int, intermediate: int, align: int = 4096) -> dict:
 def encode_bank(gate, up, down, global_mode: int = 0, stream=None):
     """A device bank from BF16 expert weights: gate and up [E, I, H], down [E, H, I] (bf16 CUDA
     tensors).  Returns (uint8 CUDA tensor holding the records, moe_nvfp4_bank)."""
+    if stream is not None:
+        with _on(stream):
+            return encode_bank(gate, up, down, global_mode)
     import torch
     E, I, H = (int(v) for v in gate.shape)
     if tuple(up.shape) != (E, I, H) or tuple(down.shape) != (E, H, I):
         raise ValueError("gate and up must be [E, I, H] and down [E, H, I]")
     lay = record_layout(H, I)
-    buf = _made_on(stream, lambda: torch.zeros(E * lay["record_stride"], dtype=torch.uint8, device=gate.device))
+    buf = torch.zeros(E * lay["record_stride"], dtype=torch.uint8, device=gate.device)
     for p, w in enumerate((gate, up, down)):
         moe_nvfp4_encode(w, buf, lay["record_stride"], lay["codes_off"][p], lay["scales_off"][p],
                          lay["global_off"][p], global_mode, stream)
@@ -699,9 +744,12 @@ class Pack:
 
     def load_bank(self, layer: int, verify: bool = False, stream=None):
         """A whole layer resident on the current device: (uint8 tensor, moe_nvfp4_bank)."""
+        if stream is not None:
+            with _on(stream):
+                return self.load_bank(layer, verify)
         import torch
         i = self.info
-        buf = _made_on(stream, lambda: torch.empty(i["experts"] * i["record_stride"], dtype=torch.uint8, device="cuda"))
+        buf = torch.empty(i["experts"] * i["record_stride"], dtype=torch.uint8, device="cuda")
         self.load(layer, buf, verify=verify, stream=stream)
         bank = make_bank(buf.data_ptr(), i["experts"], i["hidden"], i["intermediate"], i["record_stride"],
                          i["codes_off"], i["scales_off"], i["global_off"], i["global_mode"])
@@ -722,10 +770,13 @@ class Rows:
         self.handle, self.pack = h, pack
 
     def forward(self, x, logits, k: int, out=None, stream=None):
+        if stream is not None:
+            with _on(stream):
+                return self.forward(x, logits, k, out)
         import torch
         i = self.pack.info
         if out is None and isinstance(x, torch.Tensor):
-            out = _made_on(stream, lambda: torch.empty_like(x))
+            out = torch.empty_like(x)
         bank = Bank()
         bank.hidden, bank.num_experts = i["hidden"], i["experts"]
         T = _layer_args(x, logits, bank, out)
