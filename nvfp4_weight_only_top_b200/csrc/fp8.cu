@@ -126,7 +126,7 @@ int moe_nvfp4_fp8_matmul(const void* a_dev, const float* a_scales_dev, int64_t M
   p.K = K;
   p.out = out_dev;
   p.out_f32 = out_type == MOE_NVFP4_FP8_OUT_F32;
-  return done(moe::launch_fp8_matmul(p, sms, static_cast<cudaStream_t>(stream)), "fp8 matmul");
+  return done(moe::launch_fp8_matmul(p, dev, sms, static_cast<cudaStream_t>(stream)), "fp8 matmul");
 }
 
 }  // extern "C"

@@ -39,6 +39,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "tc_pair.cuh"
 
 namespace moe {
@@ -690,9 +691,17 @@ int64_t most_row_tiles(const Fp8Matmul& p, int rows) {
   return p.offsets ? (p.M + (rows - 1) * std::min<int64_t>(p.E, p.M)) / rows : (p.M + rows - 1) / rows;
 }
 
+// Clusters that run at once, 0 where the query fails (which then is no error of the call's).
+int active_clusters(const void* kern, const cudaLaunchConfig_t& cfg) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess) return n;
+  cudaGetLastError();
+  return 0;
+}
+
 // parts: CTAs that share a tile's inputs (SPLIT; else 1).
 template <int BN, bool PAIR, bool SPLIT>
-int launch_tc(const Fp8Matmul& p, int num_sms, int parts, cudaStream_t s) {
+int launch_tc(const Fp8Matmul& p, int dev, int num_sms, int parts, cudaStream_t s) {
   using C = Cfg<BN, PAIR>;
   Maps maps;
   const uint64_t da[2] = {(uint64_t)p.K, (uint64_t)p.M}, db[2] = {(uint64_t)p.K, (uint64_t)p.E * p.N};
@@ -707,10 +716,11 @@ int launch_tc(const Fp8Matmul& p, int num_sms, int parts, cudaStream_t s) {
   if (rc) return rc;
   auto kern = fp8_tc_kernel<BN, PAIR, SPLIT>;
   if (BN == 256) {                                      // what the register split draws on
-    static const int regs = [&] {
+    static PerDevice known;
+    const int regs = known.get(dev, [&] {
       cudaFuncAttributes a{};
       return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
-    }();
+    });
     if ((regs + 7) / 8 * 8 < kRegsLaunch) return -(int)cudaErrorLaunchOutOfResources;
   }
   cudaError_t err = set_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem);
@@ -732,10 +742,8 @@ int launch_tc(const Fp8Matmul& p, int num_sms, int parts, cudaStream_t s) {
   cfg.numAttrs = PAIR || SPLIT ? 2 : 1;
   int workers = num_sms;
   if (PAIR) {                                           // pairs resident at once
-    static const int pairs = [&] {
-      int n = 0;
-      return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
-    }();
+    static PerDevice known;
+    const int pairs = known.get(dev, [&] { return active_clusters(reinterpret_cast<const void*>(kern), cfg); });
     if (pairs < 1) return -(int)cudaErrorLaunchOutOfResources;
     workers = pairs;
   }
@@ -747,34 +755,25 @@ int launch_tc(const Fp8Matmul& p, int num_sms, int parts, cudaStream_t s) {
 
 // Clusters of `parts` CTAs that run at once (fewer than SMs / parts: a cluster stays within one of the GPU's groups
 // of SMs; of eight, 64 rows x 1024 x 8192 took a second wave).
-int resident_clusters(int parts) {
-  struct Table {
-    int n[kMaxParts + 1] = {};
-    Table() {
-      using C = Cfg<64, false>;
-      const auto kern = fp8_tc_kernel<64, false, true>;
-      if (set_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem) != cudaSuccess) return;
-      for (int p = 2; p <= kMaxParts; ++p) {
-        cudaLaunchConfig_t cfg{};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = p;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3((unsigned)p);
-        cfg.blockDim = dim3(C::kThreads);
-        cfg.dynamicSmemBytes = C::kSmem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n[p], kern, &cfg) != cudaSuccess) {
-          n[p] = 0;
-          cudaGetLastError();                           // a failed query is no error of the call's
-        }
-      }
-    }
-  };
-  static const Table table;
-  return table.n[parts];
+int resident_clusters(int dev, int parts) {
+  static PerDevice known[kMaxParts + 1];
+  return known[parts].get(dev, [&] {
+    using C = Cfg<64, false>;
+    const void* kern = reinterpret_cast<const void*>(fp8_tc_kernel<64, false, true>);
+    if (set_smem_limit(kern, C::kSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)parts);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return active_clusters(kern, cfg);
+  });
 }
 
 }  // namespace
@@ -794,7 +793,7 @@ cudaError_t fp8_take_status(int* v) {
 // rows, N = 2560: 10.5, two or three CTAs a tile 9.0 / 8.6; N = 512: 10.5, five 6.8; N = 1024, K = 8192: 14.7, two
 // / four / eight 11.1 / 8.4 / 8.1.  The row tiles of several experts are not known here: an expert's last is taken
 // to be half full.
-int launch_fp8_matmul(const Fp8Matmul& p, int num_sms, cudaStream_t s) {
+int launch_fp8_matmul(const Fp8Matmul& p, int dev, int num_sms, cudaStream_t s) {
   struct Form {
     int tile_m, bn;
     double fixed, lone, loaded, join;
@@ -822,7 +821,7 @@ int launch_fp8_matmul(const Fp8Matmul& p, int num_sms, cudaStream_t s) {
     }
     for (int n = 2; n <= kMaxParts && f.bn < 256; ++n) {
       const double cn = f.fixed + f.join + f.lone * part_blocks(kall, n);
-      if (cn < best && parts_ok(f.bn, n, resident_clusters(n))) {
+      if (cn < best && parts_ok(f.bn, n, resident_clusters(dev, n))) {
         best = cn;
         bn = f.bn;
         parts = n;
@@ -838,10 +837,10 @@ int launch_fp8_matmul(const Fp8Matmul& p, int num_sms, cudaStream_t s) {
   } else if (fp8_few_wanted(p, num_sms)) {
     return launch_fp8_few(p, s);
   }
-  if (bn == 256) return launch_tc<256, true, false>(p, num_sms, 1, s);
+  if (bn == 256) return launch_tc<256, true, false>(p, dev, num_sms, 1, s);
   if (bn == 128)
-    return parts > 1 ? launch_tc<128, false, true>(p, num_sms, parts, s) : launch_tc<128, false, false>(p, num_sms, 1, s);
-  return parts > 1 ? launch_tc<64, false, true>(p, num_sms, parts, s) : launch_tc<64, false, false>(p, num_sms, 1, s);
+    return parts > 1 ? launch_tc<128, false, true>(p, dev, num_sms, parts, s) : launch_tc<128, false, false>(p, dev, num_sms, 1, s);
+  return parts > 1 ? launch_tc<64, false, true>(p, dev, num_sms, parts, s) : launch_tc<64, false, false>(p, dev, num_sms, 1, s);
 }
 
 }  // namespace moe

@@ -95,7 +95,7 @@ struct Fp8Matmul {
   void* out;                // [M, N] bf16 or f32
   int out_f32;
 };
-int launch_fp8_matmul(const Fp8Matmul& p, int num_sms, cudaStream_t s);
+int launch_fp8_matmul(const Fp8Matmul& p, int dev, int num_sms, cudaStream_t s);   // dev: the current device
 // The same for up to 16 rows (fp8_rows.cu), which launch_fp8_matmul takes where it is the faster.
 bool fp8_few_wanted(const Fp8Matmul& p, int num_sms);
 int launch_fp8_few(const Fp8Matmul& p, cudaStream_t s);
