@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdio>
+#include <cstdlib>
+#include <cstring>
 
 #include "internal.h"
 #include "moe_nvfp4.h"
@@ -46,6 +48,30 @@ int check_pointers(const void* in, const void* q, const void* scales) {
   if (!al(in, 16) || !al(q, 16) || !al(scales, 4))
     return moe::api_fail(MOE_NVFP4_ERR_INVALID_ARG, "values and codes must be 16-byte aligned, scales 4-byte aligned");
   return MOE_NVFP4_OK;
+}
+
+// MOE_NVFP4_FP8_TILE, for comparisons: 64, 128 or 256, or 64xP or 128xP with P = 1..8 CTAs a tile.
+int check_tile(moe::Fp8Tile* tile) {
+  const char* s = getenv("MOE_NVFP4_FP8_TILE");
+  if (!s || !*s) return MOE_NVFP4_OK;
+  for (const int bn : {64, 128, 256}) {
+    char text[8];
+    const int n = snprintf(text, sizeof(text), "%d", bn);
+    if (strncmp(s, text, n) != 0) continue;
+    if (s[n] == 0) {
+      tile->bn = bn;
+      return MOE_NVFP4_OK;
+    }
+    if (bn < 256 && s[n] == 'x' && s[n + 1] >= '1' && s[n + 1] <= '0' + moe::kFp8MaxParts && s[n + 2] == 0) {
+      tile->bn = bn;
+      tile->parts = s[n + 1] - '0';
+      return MOE_NVFP4_OK;
+    }
+  }
+  char msg[160];
+  snprintf(msg, sizeof(msg), "MOE_NVFP4_FP8_TILE=%.40s is not 64, 128, 256, 64xP or 128xP with P in 1..%d", s,
+           moe::kFp8MaxParts);
+  return moe::api_fail(MOE_NVFP4_ERR_INVALID_ARG, msg);
 }
 
 }  // namespace
@@ -108,6 +134,8 @@ int moe_nvfp4_fp8_matmul(const void* a_dev, const float* a_scales_dev, int64_t M
   if (N < 8 || N % 8 || N > kMaxWidth)
     return moe::api_fail(MOE_NVFP4_ERR_UNSUPPORTED, "N must be a multiple of 8 in 8..65536");
   if (out_type != MOE_NVFP4_FP8_OUT_BF16 && out_type != MOE_NVFP4_FP8_OUT_F32) return bad("out_type unknown", out_type);
+  moe::Fp8Tile forced;
+  if ((rc = check_tile(&forced))) return rc;
   int dev, sms;
   if ((rc = moe::api_device(&dev, &sms))) return rc;
   if (M == 0) return MOE_NVFP4_OK;
@@ -126,7 +154,7 @@ int moe_nvfp4_fp8_matmul(const void* a_dev, const float* a_scales_dev, int64_t M
   p.K = K;
   p.out = out_dev;
   p.out_f32 = out_type == MOE_NVFP4_FP8_OUT_F32;
-  return done(moe::launch_fp8_matmul(p, dev, sms, static_cast<cudaStream_t>(stream)), "fp8 matmul");
+  return done(moe::launch_fp8_matmul(p, forced, dev, sms, static_cast<cudaStream_t>(stream)), "fp8 matmul");
 }
 
 }  // extern "C"

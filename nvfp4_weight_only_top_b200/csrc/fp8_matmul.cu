@@ -35,7 +35,6 @@
 // columns behind N fill lanes and columns that are not stored; TMA fills inputs behind K with zeros.
 #define MOE_OWN_STATUS
 #include <algorithm>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "internal.h"
@@ -52,7 +51,7 @@ constexpr int kMmaWarps = 2;
 constexpr int kMaxExperts = 1024;
 constexpr int kSuper = 8;               // row tiles taken together over the output tiles (L2 reuse)
 constexpr int kRing = 4;                // groups of four blocks' scales in shared memory
-constexpr int kMaxParts = 8;            // CTAs that share a tile (a portable cluster)
+constexpr int kMaxParts = kFp8MaxParts;
 
 template <int BN, bool PAIR>
 struct Cfg {
@@ -793,7 +792,7 @@ cudaError_t fp8_take_status(int* v) {
 // rows, N = 2560: 10.5, two or three CTAs a tile 9.0 / 8.6; N = 512: 10.5, five 6.8; N = 1024, K = 8192: 14.7, two
 // / four / eight 11.1 / 8.4 / 8.1.  The row tiles of several experts are not known here: an expert's last is taken
 // to be half full.
-int launch_fp8_matmul(const Fp8Matmul& p, int dev, int num_sms, cudaStream_t s) {
+int launch_fp8_matmul(const Fp8Matmul& p, const Fp8Tile& forced, int dev, int num_sms, cudaStream_t s) {
   struct Form {
     int tile_m, bn;
     double fixed, lone, loaded, join;
@@ -828,11 +827,9 @@ int launch_fp8_matmul(const Fp8Matmul& p, int dev, int num_sms, cudaStream_t s) 
       }
     }
   }
-  const char* env = getenv("MOE_NVFP4_FP8_TILE");       // 64, 128 or 256, 64xP or 128xP: for comparisons
-  if (env) {
-    char* end = nullptr;
-    bn = (int)strtol(env, &end, 10);
-    parts = *end == 'x' ? std::max(1, std::min(kMaxParts, atoi(end + 1))) : 1;
+  if (forced.bn) {
+    bn = forced.bn;
+    parts = forced.parts;
     while (parts > 1 && !parts_ok(bn, parts, 1 << 14)) --parts;
   } else if (fp8_few_wanted(p, num_sms)) {
     return launch_fp8_few(p, s);

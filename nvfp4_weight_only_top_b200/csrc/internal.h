@@ -95,7 +95,11 @@ struct Fp8Matmul {
   void* out;                // [M, N] bf16 or f32
   int out_f32;
 };
-int launch_fp8_matmul(const Fp8Matmul& p, int dev, int num_sms, cudaStream_t s);   // dev: the current device
+constexpr int kFp8MaxParts = 8;   // CTAs that share a tile (a portable cluster)
+struct Fp8Tile {                  // a tile taken for comparisons instead of the one that the sizes give (bn 0: none)
+  int bn = 0, parts = 1;          // 64, 128 (shared by `parts` CTAs, fewer where one would have no inputs) or 256
+};
+int launch_fp8_matmul(const Fp8Matmul& p, const Fp8Tile& forced, int dev, int num_sms, cudaStream_t s);   // dev: the current device
 // The same for up to 16 rows (fp8_rows.cu), which launch_fp8_matmul takes where it is the faster.
 bool fp8_few_wanted(const Fp8Matmul& p, int num_sms);
 int launch_fp8_few(const Fp8Matmul& p, cudaStream_t s);

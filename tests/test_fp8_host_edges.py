@@ -29,3 +29,21 @@ def test_quantize_no_rows_into_expert_order():
     for k in (0, 33):
         assert quantize(None, 0, 256, None, k, None, None, None) == BAD
     assert quantize(_p(A), 1, 256, None, 4, _p(B), _p(B), None) == BAD
+
+
+def _matmul():
+    return moe.lib().moe_nvfp4_fp8_matmul(_p(A), _p(A), 0, _p(B), _p(B), 1, 128, 256, None, _p(B), 0, None)
+
+
+@pytest.mark.parametrize("tile", ["64", "128", "256", "64x1", "64x8", "128x2", ""])
+def test_forced_tiles(tile, monkeypatch):
+    monkeypatch.setenv("MOE_NVFP4_FP8_TILE", tile)
+    assert _passes_the_checks(_matmul())
+
+
+@pytest.mark.parametrize("tile", ["wide", "32", "640", "64x", "64x0", "64x9", "64x10", "256x2", "64 ", " 64", "128X2", "-64"])
+def test_unreadable_tiles_are_refused(tile, monkeypatch):
+    """Not taken for one of the tiles."""
+    monkeypatch.setenv("MOE_NVFP4_FP8_TILE", tile)
+    assert _matmul() == BAD
+    assert "MOE_NVFP4_FP8_TILE" in moe.moe_nvfp4_last_error()
