@@ -20,6 +20,7 @@ from ._abi import Bank, MoeError, PackInfo, Router, PATH_AUTO, PATH_DECODE, PATH
 from ._abi import EP_EXPERT_MAJOR, EP_SOURCE_MAJOR  # noqa: F401
 
 _LIB = None
+_I32 = 0x7FFFFFFF       # largest size that the C calls take as int32_t; ctypes cuts larger ones off without a word
 
 
 def lib() -> ctypes.CDLL:
@@ -57,6 +58,10 @@ def _need(name: str, t, dtype, shape, device: bool = True) -> None:
         raise ValueError(f"{name} must be contiguous")
     if device and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
         raise ValueError(f"{name} must be on the current CUDA device (it is on {t.device})")
+
+
+def _too_large(name: str, v: int):
+    raise ValueError(f"{name} = {v} does not fit in 32 bits")
 
 
 def _layer_args(x, logits, bank: Bank, out, x_next=None, workspace=None, extra=()) -> int:
@@ -246,6 +251,8 @@ def moe_nvfp4_route(logits, k: int, stream=None) -> dict:
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
     T, E = (int(v) for v in logits.shape)
+    if E > _I32:
+        _too_large("E", E)
     _need("logits", logits, torch.float32, (T, E))
     dev = logits.device
     r = dict(ids=torch.empty((T, k), dtype=torch.int32, device=dev),
@@ -270,6 +277,9 @@ def make_router(score: str = "sigmoid", groups: int = 1, top_groups: int | None 
     router holds a reference to it."""
     if score not in _SCORES:
         raise ValueError(f"score {score!r} is not one of {sorted(_SCORES)}")
+    for name, v in (("groups", groups), ("top_groups", top_groups or 0), ("group_top", group_top)):
+        if not -_I32 <= v <= _I32:
+            _too_large(name, v)
     r = Router(_SCORES[score], groups, groups if top_groups is None else top_groups, group_top, int(bool(renormalize)),
                scale, None)
     r.bias = bias
@@ -301,6 +311,8 @@ def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
     T, E = logits.shape
+    if E > _I32:
+        _too_large("E", E)
     if not logits.is_cuda:
         _need("logits", logits, torch.float32, (T, E))
     dev = torch.cuda.current_device()
@@ -371,6 +383,8 @@ def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, K]")
     T, K = x.shape
+    if K > _I32 or k > _I32:
+        _too_large("K or k", max(K, k))
     dev = _fp8_in("x", x)
     if inv is not None:
         _fits("inv", inv, torch.int32, (T * k,), dev)
@@ -390,6 +404,8 @@ def moe_nvfp4_fp8_swiglu_quantize(gu, q=None, scales=None, stream=None):
         raise ValueError("gu must be a 2-D torch tensor [R, 2 I]")
     R, I = gu.shape
     I //= 2
+    if I > _I32:
+        _too_large("I", I)
     dev = _fp8_in("gu", gu)
     q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_swiglu_quantize(gu.data_ptr(), R, I, q.data_ptr(), scales.data_ptr(),
@@ -408,6 +424,8 @@ def moe_nvfp4_fp8_quantize_weights(w, q=None, scales=None, stream=None):
         raise ValueError("w must be a torch tensor [n, N, K] or [N, K]")
     shape = tuple(w.shape)
     n, N, K = (1,) * (3 - w.dim()) + shape
+    if N > _I32 or K > _I32:
+        _too_large("N or K", max(N, K))
     dev = _fp8_in("w", w)
     q, scales = _fp8_out(w, q, scales, shape, shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_quantize_weights(w.data_ptr(), n, N, K, q.data_ptr(), scales.data_ptr(),
@@ -435,6 +453,8 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
     else:
         E, N = b.shape[:2]
         shape, tiles = (E, N, K), (E, (N + 127) // 128, kb)
+    if E > _I32 or N > _I32 or K > _I32:
+        _too_large("E, N or K", max(E, N, K))
     if out is None:
         if out_dtype not in (None, torch.bfloat16, torch.float32):
             raise ValueError(f"out_dtype {out_dtype} is not torch.bfloat16 or torch.float32")
@@ -504,6 +524,8 @@ def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, H]")
     T, H = (int(v) for v in x.shape)
+    if H > _I32 or k > _I32:
+        _too_large("H or k", max(H, k))
     if rows is None:
         rows = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
     need = [("x", x, torch.bfloat16, (T, H)), ("perm", perm, torch.int32, (T * k,)),
@@ -528,6 +550,8 @@ def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=N
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         raise ValueError("y must be a 2-D torch tensor [T*k, H]")
     H = int(y.shape[1])
+    if H > _I32 or k > _I32:
+        _too_large("H or k", max(H, k))
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
     need = [("y", y, torch.float32, (T * k, H)), ("w", w, torch.float32, (T, k)), ("inv", inv, torch.int32, (T * k,)),
@@ -651,6 +675,8 @@ def moe_nvfp4_encode(w, dst, dst_stride: int, codes_off: int, scales_off: int, g
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("w must be a 3-D torch tensor [n, out, in]")
     n, out_f, in_f = (int(v) for v in w.shape)
+    if out_f > _I32 or in_f > _I32:
+        _too_large("out or in", max(out_f, in_f))
     if not isinstance(dst, torch.Tensor) or dst.dim() != 1:
         raise ValueError("dst must be a 1-D torch uint8 tensor")
     end = max(codes_off + out_f * in_f // 2, scales_off + out_f * in_f // 16, global_off + 4)

@@ -47,3 +47,34 @@ def test_unreadable_tiles_are_refused(tile, monkeypatch):
     monkeypatch.setenv("MOE_NVFP4_FP8_TILE", tile)
     assert _matmul() == BAD
     assert "MOE_NVFP4_FP8_TILE" in moe.moe_nvfp4_last_error()
+
+
+WIDE = (1 << 32) + 256             # 256 where only 32 bits are kept
+
+
+def _meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda: moe.moe_nvfp4_route(_meta(1, WIDE, dtype=torch.float32), 4),
+    lambda: moe.moe_nvfp4_route_scored(_meta(1, WIDE, dtype=torch.float32), moe.make_router(), 4),
+    lambda: moe.moe_nvfp4_fp8_quantize(_meta(1, WIDE)),
+    lambda: moe.moe_nvfp4_fp8_quantize(_meta(1, 256), inv=_meta(4, dtype=torch.int32), k=(1 << 32) + 4),
+    lambda: moe.moe_nvfp4_fp8_swiglu_quantize(_meta(1, 2 * WIDE)),
+    lambda: moe.moe_nvfp4_fp8_quantize_weights(_meta(2, WIDE, 256)),
+    lambda: moe.moe_nvfp4_fp8_quantize_weights(_meta(256, WIDE)),
+    lambda: moe.moe_nvfp4_fp8_matmul(_meta(1, WIDE), None, _meta(256, WIDE), None),
+    lambda: moe.moe_nvfp4_fp8_matmul(_meta(1, 256), None, _meta(WIDE, 256), None),
+    lambda: moe.moe_nvfp4_fp8_matmul(_meta(1, 256), None, _meta(WIDE, 8, 256), None, _meta(1, dtype=torch.int32)),
+    lambda: moe.moe_nvfp4_gather_rows(_meta(1, WIDE), _meta(2, dtype=torch.int32), 2),
+    lambda: moe.moe_nvfp4_combine(_meta(2, WIDE, dtype=torch.float32), _meta(1, 2, dtype=torch.float32), None, 2),
+    lambda: moe.moe_nvfp4_encode(_meta(1, WIDE, 256), _meta(16, dtype=torch.uint8), 0, 0, 0, 0),
+    lambda: moe.make_router(groups=(1 << 32) + 8),
+    lambda: moe.make_router(groups=8, top_groups=(1 << 32) + 4),
+    lambda: moe.make_router(groups=8, group_top=(1 << 32) + 2),
+])
+def test_sizes_past_32_bits_are_refused(call):
+    """Not taken modulo 2^32."""
+    with pytest.raises(ValueError, match="32 bits"):
+        call()
