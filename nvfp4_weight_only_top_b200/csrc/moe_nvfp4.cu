@@ -315,7 +315,8 @@ moe::RouteBufs route_bufs(uint8_t* ws, const WsLayout& L) {
 int check_k_T(int64_t T, int E, int k) {
   if (T < 0) return fail(MOE_NVFP4_ERR_INVALID_ARG, "T = %lld is negative", (long long)T);
   if (k < 1 || k > 32 || k > E) return fail(MOE_NVFP4_ERR_INVALID_ARG, "k = %d outside 1..min(E=%d, 32)", k, E);
-  if (T > ((int64_t)1 << 31) / 32) return fail(MOE_NVFP4_ERR_UNSUPPORTED, "T = %lld too large", (long long)T);
+  if (T > ((int64_t)1 << 31) / 32 || T * k >= (int64_t)1 << 31)   // offsets hold the row count in 32 bits
+    return fail(MOE_NVFP4_ERR_UNSUPPORTED, "T = %lld too large", (long long)T);
   return MOE_NVFP4_OK;
 }
 

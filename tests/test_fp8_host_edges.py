@@ -78,3 +78,19 @@ def test_sizes_past_32_bits_are_refused(call):
     """Not taken modulo 2^32."""
     with pytest.raises(ValueError, match="32 bits"):
         call()
+
+
+def _route(T, k, E=64):
+    r = moe.make_router()
+    return moe.lib().moe_nvfp4_route_scored(_p(A), T, E, ctypes.byref(r), k, *[_p(B)] * 6, None)
+
+
+def test_routed_rows_fit_32_bits():
+    """2^26 tokens of 32 choices are 2^31 rows, one more than the last offset can say."""
+    for T, k in ((1 << 26, 32), ((1 << 26) + 1, 1)):
+        assert _route(T, k) == UNS and "too large" in moe.moe_nvfp4_last_error()
+        assert moe.lib().moe_nvfp4_route(_p(A), T, 64, k, *[_p(B)] * 6, None) == UNS
+        assert "too large" in moe.moe_nvfp4_last_error()
+    if not torch.cuda.is_available():
+        for T, k in (((1 << 26) - 1, 32), (1 << 26, 31)):
+            assert _passes_the_checks(_route(T, k))
