@@ -243,7 +243,8 @@ typedef struct moe_nvfp4_router {
 
 /*
  * moe_nvfp4_route with that rule: the same outputs, laid out the same.  It takes no scratch beyond
- * its outputs, so calls on different streams and captured calls share nothing.
+ * its outputs, so calls on different streams and captured calls share nothing.  Pointers are 4-byte
+ * aligned; T k < 2^31.
  */
 int moe_nvfp4_route_scored(const float* logits_dev, int64_t T, int32_t E,
                            const moe_nvfp4_router* router, int32_t k, int32_t* ids_dev,

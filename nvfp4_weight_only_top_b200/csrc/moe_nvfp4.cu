@@ -1102,6 +1102,9 @@ int moe_nvfp4_route_scored(const float* logits_dev, int64_t T, int32_t E, const 
   if (rc) return rc;
   moe::ScoreRule rule;
   if ((rc = check_router(router, E, k, &rule))) return rc;
+  for (const void* p : {(const void*)logits_dev, (const void*)ids_dev, (const void*)w_dev, (const void*)counts_dev,
+                        (const void*)offsets_dev, (const void*)perm_dev, (const void*)inv_dev})
+    if (!aligned(p, 4)) return fail(MOE_NVFP4_ERR_INVALID_ARG, "every pointer must be 4-byte aligned");
   int dev;
   DeviceInfo info;
   if ((rc = current_device(&dev, &info))) return rc;

@@ -94,3 +94,12 @@ def test_routed_rows_fit_32_bits():
     if not torch.cuda.is_available():
         for T, k in (((1 << 26) - 1, 32), (1 << 26, 31)):
             assert _passes_the_checks(_route(T, k))
+
+
+@pytest.mark.parametrize("which", range(7))
+def test_misaligned_router_pointers_are_refused(which):
+    ptrs = [A] + [B] * 6
+    ptrs[which] += 2
+    r = moe.make_router()
+    rc = moe.lib().moe_nvfp4_route_scored(_p(ptrs[0]), 4, 64, ctypes.byref(r), 4, *[_p(v) for v in ptrs[1:]], None)
+    assert rc == BAD and "aligned" in moe.moe_nvfp4_last_error()
