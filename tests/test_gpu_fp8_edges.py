@@ -101,3 +101,84 @@ def test_an_e4m3_layer_of_no_tokens():
     torch.cuda.synchronize()
     assert q.shape == (0, H) and s.shape == (0, 2) and gu.shape == (0, 2 * I) and out.shape == (0, H)
     assert moe.moe_nvfp4_device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------ products
+
+def _codes(rng, *shape):
+    """Every finite E4M3 encoding."""
+    torch, _ = _torch()
+    c = rng.integers(0, 256, shape, dtype=np.uint8)
+    c[(c & 0x7F) == 0x7F] ^= 1
+    return torch.from_numpy(c).cuda().view(torch.float8_e4m3fn)
+
+
+def _scales(rng, *shape):
+    torch, _ = _torch()
+    return torch.from_numpy(np.exp2(rng.uniform(-9, 3, shape)).astype(np.float32)).cuda()
+
+
+def _before_nan(t):
+    """The same values in a buffer that goes on with NaNs (codes 0x7F, or f32)."""
+    torch, _ = _torch()
+    flat = t.reshape(-1)
+    if t.dtype == torch.float32:
+        buf = torch.cat([flat, torch.full((1 << 14,), float("nan"), device="cuda")])
+        return buf[:flat.numel()].view(t.shape)
+    buf = torch.cat([flat.view(torch.uint8), torch.full((1 << 16,), 0x7F, dtype=torch.uint8, device="cuda")])
+    return buf[:flat.numel()].view(t.dtype).view(t.shape)
+
+
+def _check_product(a, sa, b, sb, off, out):
+    """Against f64 products; f32 sums of 128 products (an addition loses at most 2^-23 of the magnitudes) and one
+    multiply-add a block."""
+    E, N, K = b.shape
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if r.start == r.stop:
+            continue
+        d = a[r].double() * sa[r].double().repeat_interleave(128, 1)[:, :K]
+        w = b[e].double() * sb[e].double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        tol = d.abs() @ w.abs().T * (132 + -(-K // 128)) * 2.0 ** -23
+        assert ((out[r].double() - d @ w.T).abs() <= tol).all(), e
+
+
+@pytest.mark.parametrize("tile", ["", "64", "128", "256", "64x2", "128x2"])
+@pytest.mark.parametrize("M", [13, 33, 129, 257])
+@pytest.mark.parametrize("N,K", [(40, 144), (264, 144), (264, 1296)])
+def test_nothing_behind_the_operands_enters(M, N, K, tile, monkeypatch):
+    """Codes and scales behind every operand are NaN, and so is what the call before left on the SMs: the row boxes past
+    the last row, the weight boxes past the last expert's outputs and the inputs past K reach no output."""
+    torch, moe = _torch()
+    monkeypatch.setenv("MOE_NVFP4_FP8_TILE", tile)
+    rng = np.random.default_rng(M + N + K)
+    E = 2
+    a, sa, b, sb = _codes(rng, M, K), _scales(rng, M, -(-K // 128)), _codes(rng, E, N, K), _scales(rng, E, -(-N // 128), -(-K // 128))
+    for cut in (0, M // 3, M - 1):
+        off = torch.tensor([0, cut, M], dtype=torch.int32, device="cuda")
+        nan = [torch.full_like(t.view(torch.uint8), 0x7F).view(t.dtype) for t in (a, b)]
+        left = moe.moe_nvfp4_fp8_matmul(nan[0], sa, nan[1], sb, off, out_dtype=torch.float32)
+        assert torch.isnan(left).all()
+        out = moe.moe_nvfp4_fp8_matmul(_before_nan(a), _before_nan(sa), _before_nan(b), _before_nan(sb), off,
+                                       out_dtype=torch.float32)
+        _check_product(a, sa, b, sb, off.tolist(), out)
+    assert moe.moe_nvfp4_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 8, 16, 200, 1500])
+@pytest.mark.parametrize("E", [33, 256, 1024])
+def test_products_over_many_experts(M, E):
+    """Rows of a few of up to 1024 experts, the last one among them, and of all of them."""
+    torch, moe = _torch()
+    rng = np.random.default_rng(M + E)
+    N, K = 136, 272
+    a, sa, b, sb = _codes(rng, M, K), _scales(rng, M, 3), _codes(rng, E, N, K), _scales(rng, E, 2, 3)
+    few = np.bincount(rng.choice([0, E // 2, E - 2, E - 1], M), minlength=E)
+    last = np.bincount(np.full(M, E - 1), minlength=E)
+    spread = np.bincount(rng.integers(0, E, M), minlength=E)
+    for counts in (few, last, spread):
+        off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        out = torch.full((M, N), float("nan"), device="cuda")
+        moe.moe_nvfp4_fp8_matmul(a, sa, b, sb, torch.from_numpy(off).cuda(), out=out)
+        _check_product(a, sa, b, sb, off, out)
+    assert moe.moe_nvfp4_device_status() == 0
