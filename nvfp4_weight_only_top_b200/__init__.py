@@ -293,13 +293,17 @@ def make_router(score: str = "sigmoid", groups: int = 1, top_groups: int | None 
 
 
 def _router_bias(router: Router, E: int) -> None:
-    """A router made by make_router carries its bias tensor: checks it against E and the device."""
+    """A router made by make_router carries its bias tensor: checks it against E and the device, and takes its address
+    (which assigning to bias.data changes)."""
     import torch
     if not isinstance(router, Router):
         raise ValueError("router must come from make_router")
     bias = getattr(router, "bias", None)
     if bias is not None:
         _fits("bias", bias, torch.float32, (E,), torch.cuda.current_device())
+        at = bias.data_ptr()
+        if at != router.bias_dev:
+            router.bias_dev = at
 
 
 def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:

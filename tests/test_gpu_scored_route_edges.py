@@ -65,3 +65,18 @@ def test_small_weights(score, renormalize):
         w = _route(lg, k, score=score, renormalize=renormalize, scale=scale)["w"]
         ids, want = scored.route_scored(lg, k, score=score, renormalize=renormalize, scale=scale)
         assert (np.abs(w - want) <= 64 * 2.0 ** -24 * want + 2.0 ** -149).all(), scale
+
+
+def test_a_bias_whose_storage_changes():
+    """The router reads the bias tensor as it is at the call."""
+    import torch
+    import nvfp4_weight_only_top_b200 as moe
+    lg = torch.zeros(3, 16, device="cuda")
+    bias = torch.zeros(16, device="cuda")
+    router = moe.make_router(bias=bias)
+    assert moe.moe_nvfp4_route_scored(lg, router, 2)["ids"].tolist() == [[0, 1]] * 3
+    bias.data = torch.arange(16, dtype=torch.float32, device="cuda")
+    assert moe.moe_nvfp4_route_scored(lg, router, 2)["ids"].tolist() == [[15, 14]] * 3
+    bias.data = torch.zeros(8, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_nvfp4_route_scored(lg, router, 2)
