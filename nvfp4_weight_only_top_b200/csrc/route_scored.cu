@@ -710,7 +710,11 @@ int launch_scored(const float* logits, int64_t T, int E, int k, const ScoreRule&
     return err == cudaSuccess ? 1 : -(int)err;
   }
   const bool few = T * k <= kFewRows;
-  const int warps = few && T > 512 ? kChoiceWarps : 4;   // (1024 tokens 9.3 us, with four 12.8; 512 7.8, with eight 8.3)
+  // A CTA's tokens: four, but eight from 513 to 1024 tokens before the counting placement.  Both sides in a graph, four /
+  // eight (us), 256 experts, k = 8: 64 tokens 6.6 / 7.0, 512 8.0 / 8.5, 768 11.5 / 9.0, 1024 12.9 / 9.5, 1365 12.1 / 12.6,
+  // 8192 19.8 / 20.5, 32768 47.5 / 49.0; 64 of softmax, k = 6: 768 9.6 / 8.1, 1024 10.2 / 8.3, 1365 11.3 / 11.3, 8192
+  // 15.6 / 16.0; 512, k = 2: 768 9.6 / 9.9, 1024 10.7 / 10.0, 1365 12.3 / 13.9, 4096 21.1 / 23.3, 32768 77 / 82.
+  const int warps = few && T > 512 && T <= 1024 ? kChoiceWarps : 4;
   scored_choice_kernel<PER><<<(unsigned)((T + warps - 1) / warps), 32 * warps, 0, s>>>(logits, T, E, k, r, b);
   if (few) {
     const int R = (int)(T * k);
