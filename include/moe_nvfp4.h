@@ -270,17 +270,19 @@ int moe_nvfp4_forward_scored(const void* x_dev, const float* logits_dev, int64_t
  * (tiles at the right and lower edge hold what is left).  The quantizers form, in f32,
  *   m = max(max |v| of the block, 2^-100),  scale = m / 448,  code = e4m3(v * (448 / m)),
  * nearest even.  A block with a NaN gets a NaN scale and codes, one with an infinity an infinite scale
- * (every product with it is then NaN).  A product takes the two scales' product in f32.  K (I for SwiGLU) is a multiple of 16 up to 65536; pointers to
- * BF16 and E4M3 data are 16-byte aligned, scales and indices 4-byte.  None of these calls takes
- * scratch.
+ * (every product with it is then NaN).  A product takes the two scales' product in f32.  K (I for
+ * SwiGLU) is a multiple of 16 up to 65536; pointers to BF16 and E4M3 data are 16-byte aligned, scales
+ * and indices 4-byte.  None of these calls takes scratch.
  *
  * moe_nvfp4_fp8_quantize         x_dev [T, K] BF16.  inv_dev NULL and k = 1: row t to row t.  Else
  *     inv_dev [T*k] int32 and 1 <= k <= 32: row t to the k rows inv[t*k + j] of q_dev [T*k, K] --
- *     with a router's inv, the routed rows in expert order.  An entry outside [0, T*k) is skipped.
+ *     with a router's inv, the routed rows in expert order.  An entry outside [0, T*k) is skipped; the
+ *     others are distinct (a row that two of them name is left with codes and scales of either).
  *     With T = 0 inv_dev may be NULL for every k.
  * moe_nvfp4_fp8_swiglu_quantize  gu_dev [R, 2 I] BF16, gate in columns 0 .. I-1 and up behind it:
  *     q_dev [R, I], scales_dev [R, ceil(I/128)] of silu(gate) * up = gate / (1 + exp(-gate)) * up.
- *     Codes from 2^-6 on are those of 64 bits; smaller ones and the scales are formed in f32.
+ *     Codes from 2^-6 on are those of 64 bits, for every finite gate and up; smaller ones and the
+ *     scales are formed in f32, within 6 x 2^-23 of the latter.
  * moe_nvfp4_fp8_quantize_weights w_dev [n, N, K] BF16, n <= 65535, N <= 1048576.
  */
 int moe_nvfp4_fp8_quantize(const void* x_dev, int64_t T, int32_t K, const int32_t* inv_dev,

@@ -25,7 +25,7 @@ INPUTS_LIB = os.path.join(ROOT, "moe_inputs", "libmoe_inputs.so")
 
 # Sources compiled on their own, which share no device symbols with the others: in relocatable device code
 # setmaxnreg (a register split between warps, fp8_matmul.cu) is ignored, and a kernel that calls a function that
-# is not inlined gets the registers that the function would like (route_scored.cu: 110, where two CTAs an SM
+# is not inlined gets the registers that the function would like (route_scored.cu: 110, where its launch bounds
 # leave 64; fp8_quant.cu).
 WHOLE = {"fp8_matmul.cu", "fp8_quant.cu", "route_scored.cu"}
 

@@ -22,10 +22,12 @@
 // A pair (cta_group::2) shares the weights: each CTA loads half of the BN weight rows and its own 128
 // rows, 32 KB a block instead of 48, which the L2 can deliver in the time of the MMAs (512 clocks).
 //
-// Measured: 65787 rows over 32 experts x 5120 x 5120 1.62 ms, 2.13 PFLOP/s (0.77 of twice the measured sustained BF16
-// rate), at the 1000 W power cap and about 1.5 GHz; without its multiply-adds the same kernel takes 1.3 ms: they fill
-// a quarter of the issue slots, and a wait for an accumulator, its loads and they are one chain a warp.  Decode
-// batches read the weights: 67 rows over 32 experts x 5120 x 5120 88 us, the live experts' 740 MB at the memory's rate.
+// Measured: 65787 rows over 32 experts x 5120 x 5120.  A few calls: 1.61 ms, 2.14 PFLOP/s, 0.65 of twice the measured
+// burst BF16 rate.  Six seconds of calls: 1.88 ms each at 990 W (the power cap) and 1380 MHz, 1.83 PFLOP/s, 0.67 of
+// twice the sustained BF16 rate.  Without its multiply-adds the same kernel takes 1.3 ms in a few calls: they fill a
+// quarter of the issue slots, and a wait for an accumulator, its loads and they are one chain a warp (tensor pipe busy
+// 62 %, issue slots 65 %: neither is full).  Decode batches read the weights: 67 rows over 32 experts x 5120 x 5120
+// with 19 of them live 87 us, 490 MB at 0.86 of the measured copy's rate.
 //
 // Few tiles of long rows are shared by a cluster of up to eight CTAs, each a run of the blocks: with one CTA a tile
 // the chain of its blocks is the time (64 rows x 512 x 5120: 10.5 us, five CTAs a tile 6.8).  Each leaves its sums in
@@ -788,7 +790,9 @@ cudaError_t fp8_take_status(int* v) {
 // measurements (us): a lone wave's blocks are bound by one CTA's chain of steps, more waves' by the L2's rate.  Tiles
 // shared by a cluster of CTAs, for calls of a few tiles and long rows, pay for joining the sums.  Both sides
 // measured, K = 5120 (us; 64 / 128 / pair): 64 rows, N = 5120: 10.9 / 13.1 / 20.5; 256 rows: 20.6 / 13.8 / 21.6;
-// 4096 rows: 156 / 111 / 100; 2048 rows over 32 experts: 206 / 145 / 197; 65787 over 32: 2779 / 1792 / 1597; 64
+// 4096 rows: 156 / 111 / 100; 2048 rows over 32 experts: 206 / 145 / 197; 8192 over 32: 396 / 298 / 297 (256 rows an
+// expert, many of which take two of the pair's tiles; the estimate, 225 and 220, leaves that out on both sides); 65536
+// over 256: 3785 / 2473 / 2937; 65787 over 32: 2779 / 1792 / 1597; 64
 // rows, N = 2560: 10.5, two or three CTAs a tile 9.0 / 8.6; N = 512: 10.5, five 6.8; N = 1024, K = 8192: 14.7, two
 // / four / eight 11.1 / 8.4 / 8.1.  The row tiles of several experts are not known here: an expert's last is taken
 // to be half full.

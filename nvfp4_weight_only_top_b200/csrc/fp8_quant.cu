@@ -8,10 +8,11 @@
 // number; a block of zeros gets zero codes.  A NaN in a block, or an infinity, makes every product
 // with the block NaN (scale NaN and codes NaN, or scale infinite and codes 0 or NaN).
 //
-// One pass over the data: a thread holds 16 values of a block (two 16-byte loads, one 16-byte
-// store), eight threads a row block, and the block's maximum is a butterfly over them.  The SiLU takes the
-// hardware exponential and reciprocal (with the exact ones the arithmetic, not the memory, set the time); where a
-// product lies nearer to the border between two codes than that can be off, 64 bits decide.
+// One pass over the data: a thread holds 16 values of a block (one 32-byte load, or two of 16 bytes where the rows
+// start off a 32-byte boundary; one 16-byte store), eight threads a row block, and the block's maximum is a butterfly
+// over them.  The SiLU takes the hardware exponential and reciprocal (with the exact ones the arithmetic, not the
+// memory, set the time); where a product lies nearer to the border between two codes than that can be off, or a block
+// has an up that can outweigh what they lose of a far negative gate, 64 bits decide.
 #define MOE_OWN_STATUS
 #include "common.cuh"
 #include "internal.h"
@@ -158,8 +159,9 @@ __device__ __noinline__ void settle(const uint16_t* gate, const uint16_t* up, bo
 // Thread u of the flat list handles 16-value chunk u % 8 of block (u / 8) % KB of row u / (8 KB).  Bound by memory
 // with enough loads under way, which is a matter of resident threads, and with SwiGLU nearly by the issue slots: 12
 // CTAs of 128 an SM (40 registers; ten 157 us), 32-byte loads (of 16 bytes, a warp's touch every sector twice: 3 us
-// more), no 64-bit division (16 us).  65787 x 2560 outputs 147 us (5.8 TB/s, 0.88 of the measured copy).  Without
-// SwiGLU 71 us into expert order at 8192 x 5120, k = 8 (6.1 TB/s, 0.93).
+// more), no 64-bit division (16 us).  65787 x 2560 outputs in a graph 148 us (5.7 TB/s, 0.87 of the measured copy),
+// called one by one 153 to 180 (outputs made anew, other inputs).  Without SwiGLU in a graph 71 us into expert order
+// at 8192 x 5120, k = 8 (6.1 TB/s, 0.93).
 template <bool SWIGLU, bool WIDE>
 __global__ void __launch_bounds__(kRowThreads, SWIGLU ? 12 : 8) fp8_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int K, int kb, uint64_t kb_inv,
                                                        const int32_t* __restrict__ inv, int k, int64_t limit,

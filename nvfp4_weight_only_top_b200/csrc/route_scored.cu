@@ -15,7 +15,7 @@
 // a choice lie within one step of 32 bits of each other in almost every call, and the rounding of
 // the exponential would then decide.  A token is chosen for in 32 bits first; where two of the
 // values that decide lie nearer to each other than those 32 bits can be off, or anything is not
-// finite, 64 bits decide.
+// finite, 64 bits decide.  Weights are formed in 32 bits, and in 64 where they come near the end of those.
 //
 // The kernels keep nothing between calls and use no scratch: the rows per expert of each chunk of
 // tokens wait in the chunk's own part of inv (at least E ints long by the choice of the chunk)
@@ -23,14 +23,16 @@
 // streams, or captured into graphs, therefore share nothing.
 //
 // What bounds it: one call's bytes (8192 tokens of 256 experts: 9.4 MB, 1.4 us) are nothing beside the chain
-// load - choice - counts - placement of a token and, with many tokens, the issue of about 960 instructions a token
-// (8192 tokens: the choice takes about half of the time).  So: one launch and one CTA up to 8 tokens; a choice
+// load - choice - counts - placement of a token.  With many tokens it is that chain still: a warp walks one token's
+// rounds of the choice one after another, about 890 instructions a token, and 64 registers leave 32 warps an SM to
+// fill its waits (4096 tokens: issue slots busy 47 %, 36 % of the warps resident; 8192: the choice takes about half
+// of the time).  So: one launch and one CTA up to 8 tokens; a choice
 // over CTAs of a few tokens and a placement that counts the call's ids itself up to 8192 rows; above, the choice,
 // counts per chunk, a scan over the chunks and the placement, each set up while the one before runs.  (Counting in
 // the choice saves a launch, but chunks that hold their counts are long where experts are many: 32768 tokens of
 // 1024 experts, k = 1, 1108 us, now 256; 8192, k = 4, 295, now 82; 1025 of 256, k = 8, 16.1, now 11.2.)
-// Measured in a graph, 256 experts in 8 groups, k = 8 (us; in brackets the neighbouring way): 1 token 4.0,
-// 8 5.0 (5.5), 16 5.6 (6.5), 67 6.8, 512 7.8 (13.8), 1024 9.3, 8192 20 (44).
+// Measured in a graph, 256 experts in 8 groups, k = 8 (us; in brackets the neighbouring way): 1 token 4.1,
+// 8 5.0 (5.5), 16 5.6 (6.5), 67 6.8, 512 8.0 (13.8), 1024 9.6, 8192 20 (44).
 #define MOE_OWN_STATUS
 #include <algorithm>
 
