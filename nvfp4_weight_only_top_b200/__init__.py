@@ -103,23 +103,31 @@ def _fits(name: str, t, dtype, shape, dev: int) -> None:
         _need(name, t, dtype, shape)
 
 
-def _raw_stream(dev: int) -> int:
-    """The current stream of the device."""
+def _raw_stream(stream, dev: int) -> int:
     import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream):
-    """The context of a call with a stream: it runs, and allocates its outputs, on that one.  (Made on the stream that is
-    current, they could be memory that its work still reads, or be given out again while `stream` still writes them.)"""
+def _under(stream, call, *args):
+    """call(*args) with `stream` the current stream: for a call that allocates its outputs.  (Made on the stream that is
+    current, they could be memory that its work still reads, or be given out again while `stream` still writes them.)
+    torch.cuda.stream() does the same in 7 us, a call's own host time."""
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    return torch.cuda.stream(stream)
+    dev = torch.cuda.current_device()
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be on the current CUDA device {dev} (it is on device {stream.device_index})")
+    was = torch._C._cuda_getCurrentStream(dev)
+    torch._C._cuda_setStream(stream_id=stream.stream_id, device_index=dev, device_type=stream.device_type)
+    try:
+        return call(*args)
+    finally:
+        torch._C._cuda_setStream(stream_id=was[0], device_index=was[1], device_type=was[2])
 
 
 def make_bank(base_ptr: int, num_experts: int, hidden: int, intermediate: int, record_stride: int,
@@ -136,9 +144,8 @@ def make_bank(base_ptr: int, num_experts: int, hidden: int, intermediate: int, r
 
 def moe_nvfp4_forward(x, logits, bank: Bank, k: int, out=None, stream=None):
     """out [T, H] bf16 = MoE(x [T, H] bf16, logits [T, E] f32) on the current device."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_forward(x, logits, bank, k, out)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_forward, x, logits, bank, k, out)
     import torch
     if out is None and isinstance(x, torch.Tensor):
         out = torch.empty_like(x)
@@ -151,9 +158,8 @@ def moe_nvfp4_forward(x, logits, bank: Bank, k: int, out=None, stream=None):
 def moe_nvfp4_forward_ex(x, logits, bank: Bank, k: int, out=None, x_next=None, workspace=None,
                          path: int = PATH_AUTO, stream=None):
     """As moe_nvfp4_forward, with optional residual output, caller workspace and path."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_forward_ex(x, logits, bank, k, out, x_next, workspace, path)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_forward_ex, x, logits, bank, k, out, x_next, workspace, path)
     import torch
     if out is None and isinstance(x, torch.Tensor):
         out = torch.empty_like(x)
@@ -170,9 +176,8 @@ def moe_nvfp4_forward_w4a4(x, logits, bank: Bank, act_scales, k: int, out=None, 
     expert's input multipliers of gate/up and of down.  taps, if given, maps any of "x_codes"
     [T*k, H/2] u8, "x_scales" [T*k, H/16] u8, "h" [T*k, I] f32, "h_codes" [T*k, I/2] u8 and
     "h_scales" [T*k, I/16] u8 (device tensors) to outputs filled in slot order."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_forward_w4a4(x, logits, bank, act_scales, k, out, x_next, workspace, taps)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_forward_w4a4, x, logits, bank, act_scales, k, out, x_next, workspace, taps)
     import torch
     if out is None and isinstance(x, torch.Tensor):
         out = torch.empty_like(x)
@@ -206,9 +211,8 @@ def moe_nvfp4_forward_noalloc(x, logits, bank: Bank, k: int, out=None, stream=No
     For callers that cannot allocate device memory during a call; `out` may be passed in so
     that the call itself allocates nothing on the Python side either.
     """
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_forward_noalloc(x, logits, bank, k, out)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_forward_noalloc, x, logits, bank, k, out)
     import torch
     if out is None and isinstance(x, torch.Tensor):
         out = torch.empty_like(x)
@@ -245,8 +249,7 @@ def moe_nvfp4_forward_host(x_host: np.ndarray, logits_host: np.ndarray, bank: Ba
 def moe_nvfp4_route(logits, k: int, stream=None) -> dict:
     """Routing only: ids, w, counts, offsets, perm, inv (int32 / f32 CUDA tensors)."""
     if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_route(logits, k)
+        return _under(stream, moe_nvfp4_route, logits, k)
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
@@ -309,8 +312,7 @@ def _router_bias(router: Router, E: int) -> None:
 def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
     """Scored routing (include/moe_nvfp4.h): ids, w, counts, offsets, perm, inv, as moe_nvfp4_route."""
     if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_route_scored(logits, router, k)
+        return _under(stream, moe_nvfp4_route_scored, logits, router, k)
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D torch tensor [T, E]")
@@ -332,16 +334,15 @@ def moe_nvfp4_route_scored(logits, router: Router, k: int, stream=None) -> dict:
     perm, inv, counts, offsets = buf.split_with_sizes((R, R, E, E + 1))
     at = buf.data_ptr()
     _check(lib().moe_nvfp4_route_scored(logits.data_ptr(), T, E, ctypes.byref(router), k, ids.data_ptr(), w.data_ptr(),
-                                        at + 8 * R, at + 8 * R + 4 * E, at, at + 4 * R, _raw_stream(dev)))
+                                        at + 8 * R, at + 8 * R + 4 * E, at, at + 4 * R, _raw_stream(stream, dev)))
     return dict(ids=ids, w=w, counts=counts, offsets=offsets, perm=perm, inv=inv)
 
 
 def moe_nvfp4_forward_scored(x, logits, bank: Bank, router: Router, k: int, out=None, x_next=None, workspace=None,
                              path: int = PATH_AUTO, stream=None):
     """moe_nvfp4_forward_ex with the scored router."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_forward_scored(x, logits, bank, router, k, out, x_next, workspace, path)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_forward_scored, x, logits, bank, router, k, out, x_next, workspace, path)
     import torch
     if out is None and isinstance(x, torch.Tensor):
         out = torch.empty_like(x)
@@ -380,9 +381,8 @@ def _fp8_in(name: str, x):
 def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=None):
     """x [T, K] bf16 to E4M3 codes q [T*k, K] and f32 scales [T*k, ceil(K/128)], one scale per 128
     inputs.  inv [T*k] int32 (a router's): row t goes to the rows inv[t*k + j], the expert order."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_fp8_quantize(x, inv, k, q, scales)
+    if stream is not None and (q is None or scales is None):
+        return _under(stream, moe_nvfp4_fp8_quantize, x, inv, k, q, scales)
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, K]")
@@ -394,15 +394,14 @@ def moe_nvfp4_fp8_quantize(x, inv=None, k: int = 1, q=None, scales=None, stream=
         _fits("inv", inv, torch.int32, (T * k,), dev)
     q, scales = _fp8_out(x, q, scales, (T * k, K), (T * k, (K + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_quantize(x.data_ptr(), T, K, _addr(inv), k, q.data_ptr(), scales.data_ptr(),
-                                        _raw_stream(dev)))
+                                        _raw_stream(stream, dev)))
     return q, scales
 
 
 def moe_nvfp4_fp8_swiglu_quantize(gu, q=None, scales=None, stream=None):
     """silu(gate) * up of gu [R, 2 I] bf16 (gate first), quantized: q [R, I] and scales [R, ceil(I/128)]."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_fp8_swiglu_quantize(gu, q, scales)
+    if stream is not None and (q is None or scales is None):
+        return _under(stream, moe_nvfp4_fp8_swiglu_quantize, gu, q, scales)
     import torch
     if not isinstance(gu, torch.Tensor) or gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must be a 2-D torch tensor [R, 2 I]")
@@ -413,16 +412,15 @@ def moe_nvfp4_fp8_swiglu_quantize(gu, q=None, scales=None, stream=None):
     dev = _fp8_in("gu", gu)
     q, scales = _fp8_out(gu, q, scales, (R, I), (R, (I + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_swiglu_quantize(gu.data_ptr(), R, I, q.data_ptr(), scales.data_ptr(),
-                                               _raw_stream(dev)))
+                                               _raw_stream(stream, dev)))
     return q, scales
 
 
 def moe_nvfp4_fp8_quantize_weights(w, q=None, scales=None, stream=None):
     """w [n, N, K] (or [N, K]) bf16 to E4M3 codes and f32 scales [n, ceil(N/128), ceil(K/128)], one per
     128 x 128 tile."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_fp8_quantize_weights(w, q, scales)
+    if stream is not None and (q is None or scales is None):
+        return _under(stream, moe_nvfp4_fp8_quantize_weights, w, q, scales)
     import torch
     if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
         raise ValueError("w must be a torch tensor [n, N, K] or [N, K]")
@@ -433,7 +431,7 @@ def moe_nvfp4_fp8_quantize_weights(w, q=None, scales=None, stream=None):
     dev = _fp8_in("w", w)
     q, scales = _fp8_out(w, q, scales, shape, shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dev)
     _check(lib().moe_nvfp4_fp8_quantize_weights(w.data_ptr(), n, N, K, q.data_ptr(), scales.data_ptr(),
-                                                _raw_stream(dev)))
+                                                _raw_stream(stream, dev)))
     return q, scales
 
 
@@ -441,9 +439,8 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
     """out [M, N] = the block-scaled products of a [M, K] with b [E, N, K] (or [N, K]), E4M3 both: rows
     offsets[e] .. offsets[e+1]-1 with b[e].  offsets [E+1] int32, or None for one weight and all rows.
     out_dtype torch.bfloat16 (the default) or torch.float32."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets, out, out_dtype)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_fp8_matmul, a, a_scales, b, b_scales, offsets, out, out_dtype)
     import torch
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a must be a 2-D torch tensor [M, K]")
@@ -482,7 +479,7 @@ def moe_nvfp4_fp8_matmul(a, a_scales, b, b_scales, offsets=None, out=None, out_d
         _fits("offsets", offsets, torch.int32, (E + 1,), dev)
     _check(lib().moe_nvfp4_fp8_matmul(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E, N, K,
                                       _addr(offsets), out.data_ptr(), _abi.FP8_OUT_F32 if f32 else _abi.FP8_OUT_BF16,
-                                      _raw_stream(dev)))
+                                      _raw_stream(stream, dev)))
     return out
 
 
@@ -491,9 +488,8 @@ def moe_nvfp4_experts(x_rows, expert_ids, bank: Bank, y_rows=None, workspace=Non
     """y_rows [R, H] f32 = expert expert_ids[r] applied to x_rows[r] (bf16 [R, H]); ids outside
     [0, E) are padding rows (zero output).  sorted_ids: the caller knows the ids are
     non-decreasing and all valid (MOE_NVFP4_EXPERTS_SORTED)."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_experts(x_rows, expert_ids, bank, y_rows, workspace, path, sorted_ids)
+    if stream is not None and y_rows is None:
+        return _under(stream, moe_nvfp4_experts, x_rows, expert_ids, bank, y_rows, workspace, path, sorted_ids)
     import torch
     if not isinstance(x_rows, torch.Tensor) or x_rows.dim() != 2:
         raise ValueError("x_rows must be a 2-D torch tensor [R, H]")
@@ -521,9 +517,8 @@ def moe_nvfp4_experts_workspace_bytes(R: int, E: int, H: int, I: int, path: int 
 
 def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
     """rows [T*k, H] bf16 = x[perm[p] // k]: the routed rows in expert order."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_gather_rows(x, perm, k, rows)
+    if stream is not None and rows is None:
+        return _under(stream, moe_nvfp4_gather_rows, x, perm, k, rows)
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor [T, H]")
@@ -544,9 +539,8 @@ def moe_nvfp4_gather_rows(x, perm, k: int, rows=None, stream=None):
 
 def moe_nvfp4_combine(y, w, inv, k: int, out=None, x=None, x_next=None, stream=None):
     """out [T, H] bf16 = bf16(sum_j w[t, j] * y[inv[t*k+j]]), y f32 [T*k, H] in expert order."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_combine(y, w, inv, k, out, x, x_next)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_combine, y, w, inv, k, out, x, x_next)
     import torch
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a 2-D torch tensor [T, k]")
@@ -575,8 +569,7 @@ def moe_nvfp4_ep_plan(counts_all, rank: int, recv_rows: int, layout: int = _abi.
     """From counts_all [G, E] int32 (row s = rank s's routed rows per expert): dst_off [E] and
     recv_ids [recv_rows] (int32 CUDA tensors), as include/moe_nvfp4.h describes."""
     if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_ep_plan(counts_all, rank, recv_rows, layout)
+        return _under(stream, moe_nvfp4_ep_plan, counts_all, rank, recv_rows, layout)
     import torch
     if not isinstance(counts_all, torch.Tensor) or counts_all.dim() != 2:
         raise ValueError("counts_all must be a 2-D torch tensor [G, E]")
@@ -621,9 +614,8 @@ def moe_nvfp4_ep_combine(route: dict, dst_off, recv_y_ptrs, hidden: int, capacit
     """out [T, H] bf16 = the layer's combine of the routed rows' expert outputs, read from their
     owners' f32 output buffers (recv_y_ptrs: G device addresses valid in this process, each of
     capacity_rows rows)."""
-    if stream is not None:
-        with _on(stream):
-            return moe_nvfp4_ep_combine(route, dst_off, recv_y_ptrs, hidden, capacity_rows, out, x, x_next)
+    if stream is not None and out is None:
+        return _under(stream, moe_nvfp4_ep_combine, route, dst_off, recv_y_ptrs, hidden, capacity_rows, out, x, x_next)
     import torch
     T, k = (int(v) for v in route["ids"].shape)
     E = int(dst_off.shape[0])
@@ -712,8 +704,7 @@ def encode_bank(gate, up, down, global_mode: int = 0, stream=None):
     """A device bank from BF16 expert weights: gate and up [E, I, H], down [E, H, I] (bf16 CUDA
     tensors).  Returns (uint8 CUDA tensor holding the records, moe_nvfp4_bank)."""
     if stream is not None:
-        with _on(stream):
-            return encode_bank(gate, up, down, global_mode)
+        return _under(stream, encode_bank, gate, up, down, global_mode)
     import torch
     E, I, H = (int(v) for v in gate.shape)
     if tuple(up.shape) != (E, I, H) or tuple(down.shape) != (E, H, I):
@@ -775,8 +766,7 @@ class Pack:
     def load_bank(self, layer: int, verify: bool = False, stream=None):
         """A whole layer resident on the current device: (uint8 tensor, moe_nvfp4_bank)."""
         if stream is not None:
-            with _on(stream):
-                return self.load_bank(layer, verify)
+            return _under(stream, self.load_bank, layer, verify)
         import torch
         i = self.info
         buf = torch.empty(i["experts"] * i["record_stride"], dtype=torch.uint8, device="cuda")
@@ -800,9 +790,8 @@ class Rows:
         self.handle, self.pack = h, pack
 
     def forward(self, x, logits, k: int, out=None, stream=None):
-        if stream is not None:
-            with _on(stream):
-                return self.forward(x, logits, k, out)
+        if stream is not None and out is None:
+            return _under(stream, self.forward, x, logits, k, out)
         import torch
         i = self.pack.info
         if out is None and isinstance(x, torch.Tensor):

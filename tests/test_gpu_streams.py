@@ -93,3 +93,38 @@ def test_outputs_dropped_while_the_stream_runs():
             torch.full((n,), 99, dtype=dtype, device="cuda")
     st.synchronize()
     assert np.isclose(float(total), 200 * want, rtol=1e-12)
+
+
+def test_a_refused_call_leaves_the_current_stream():
+    torch, moe, calls, _keep = _setup()
+    st, home = torch.cuda.Stream(), torch.cuda.Stream()
+    lg = torch.zeros(2, E, device="cuda")
+    with torch.cuda.stream(home):
+        with pytest.raises(ValueError):
+            moe.moe_nvfp4_route_scored(lg, moe.make_router(), 40, stream=st)
+        with pytest.raises(moe.MoeError):
+            moe.moe_nvfp4_route(lg, 40, stream=st)
+        assert torch.cuda.current_stream() == home
+        calls["route"](st)
+        assert torch.cuda.current_stream() == home
+    torch.cuda.synchronize()
+
+
+def test_given_outputs_are_written_on_the_stream():
+    """Outputs of the caller's: the call is the stream's, in order behind the work that is on it."""
+    torch, moe, _calls, _keep = _setup()
+    st = torch.cuda.Stream()
+    x = torch.zeros(64, 1024, dtype=torch.bfloat16, device="cuda")
+    q = torch.empty(64, 1024, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(64, 8, device="cuda")
+    y = torch.empty(64, 1024, dtype=torch.float8_e4m3fn, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for v in (1.0, 2.0, 3.0):
+            torch.cuda._sleep(2_000_000)
+            x.fill_(v)
+    moe.moe_nvfp4_fp8_quantize(x, q=q, scales=s, stream=st)
+    with torch.cuda.stream(st):
+        y.copy_(q)
+    st.synchronize()
+    assert (s == torch.tensor(3.0) / 448).all() and (y.float() == 448).all()
